@@ -303,6 +303,64 @@ MOE_API int moe_expert_ffn(const moe_desc* desc, const void* x, const void* w13,
 MOE_API int moe_quantize_act(const moe_desc* desc, const void* x, uint8_t* codes,
                              uint8_t* exps, void* stream);
 
+/* ---- dense products beside the experts ---- */
+
+/* Activation of moe_linear's epilogue. */
+#define MOE_FN_NONE 0
+#define MOE_FN_RELU 1
+#define MOE_FN_SILU 2       /* z / (1 + e^-z)                                  */
+#define MOE_FN_GELU 3       /* z * (normal distribution function of z)         */
+#define MOE_FN_GELU_TANH 4  /* its form with tanh(sqrt(2/pi)(z + 0.044715 z^3)) */
+
+/* A dense product with its epilogue (a shared expert, a dense feed-forward
+ * layer or a projection next to the routed experts):
+ *   z   = (x . W^T) * scale + bias           [M, R], sums in fp32
+ *   y   = fn(z)                              R = N
+ *         fn(z[:, :N]) * z[:, N:]            R = 2N, gated (rows 0..N-1 of W
+ *                                            the gate projection, N..2N-1 up)
+ *   out = y + residual                       [M, N], rounded once
+ *   x        [M, K] act dtype      W     [R, K] weight dtype
+ *   scale    [R] or [1] fp32       bias  [R] fp32 or NULL
+ *   residual [M, N] act dtype or NULL        out [M, N] act dtype
+ * The (act, weight) pairs and e4m3fn scales are the layer's (scale_mode
+ * MOE_SCALE_PER_TENSOR: one scale for the whole of W).  x, W, residual and out
+ * may have rows longer in memory than their length (ld*, in elements); any M,
+ * N and K, and any row stride, aligned or not, is accepted (the buffers
+ * themselves are 16-byte aligned).
+ * Limits: 0 <= M <= 2^28, 1 <= N <= 2^20, 1 <= K <= 2^20, M * N <= 2^34, row
+ * strides at most 2^20 (longer than the row, or 0 for dense rows). */
+typedef struct moe_linear_desc {
+  int64_t rows;          /* M                                */
+  int64_t out_features;  /* N                                */
+  int64_t in_features;   /* K                                */
+  int64_t ldx;           /* elements between rows; 0 = dense */
+  int64_t ldw;
+  int64_t ldr;
+  int64_t ldo;
+  int32_t act_dtype;     /* MOE_DTYPE_F32 / _BF16            */
+  int32_t weight_dtype;  /* MOE_DTYPE_F32 / _BF16 / _E4M3FN  */
+  int32_t fn;            /* MOE_FN_*                         */
+  int32_t gated;         /* 0 or 1                           */
+  int32_t scale_mode;    /* MOE_SCALE_*                      */
+  int32_t reserved;      /* must be 0                        */
+} moe_linear_desc;
+
+/* Bytes of device workspace moe_linear needs for `desc` (0 for most shapes:
+ * only products whose K is split over workgroups use any). */
+MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* bytes);
+
+/* The product above on `stream`.  `scale` is required for e4m3fn weights and
+ * NULL otherwise; bias and residual may be NULL.  out may be the residual
+ * itself (same address and row stride); otherwise out overlaps no input.
+ * The elements of out's rows past N are left as they are.  `workspace`:
+ * moe_linear_workspace_bytes(desc) bytes, 256-byte aligned (may be NULL when
+ * that is 0).  The result does not depend on what else runs, nor on the run:
+ * every sum has a fixed order.  Kernel timing (moe_timing_enable) covers the
+ * layer's kernels, not this one. */
+MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
+                       const float* scale, const float* bias, const void* residual, void* out,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
 /* A captured forward: moe_forward's launch sequence for one desc and one
  * set of buffers, recorded once into a HIP graph and replayed with a single
  * launch per step.  The pages' fused operation replaces a sequence of

@@ -40,6 +40,7 @@ ENTRY_POINTS = (
     "moe_route_logits", "moe_align", "moe_route_align", "moe_expert_ffn",
     "moe_quantize_act", "moe_graph_create", "moe_graph_launch", "moe_graph_destroy", "moe_strerror",
     "moe_timing_enable", "moe_timing_collect", "moe_kernel_name", "moe_forward_noalloc",
+    "moe_linear_workspace_bytes", "moe_linear",
 )
 MOE_ERR_NOALLOC_SIZE = -10
 MOE_NOALLOC_WORKSPACE_BYTES = 64 << 20
@@ -56,6 +57,14 @@ class moe_desc(ctypes.Structure):
 class moe_scales(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("w13", ctypes.c_void_p), ("w2", ctypes.c_void_p)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("out_features", ctypes.c_int64),
+                ("in_features", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldo", ctypes.c_int64), ("act_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("fn", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("scale_mode", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoEError(RuntimeError):
@@ -78,6 +87,7 @@ def lib() -> ctypes.CDLL:
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(moe_desc)
     S = ctypes.POINTER(moe_scales)
+    LD = ctypes.POINTER(moe_linear_desc)
     sig = {
         "moe_align_capacity": (I32, [D, I32, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(I64)]),
         "moe_workspace_bytes": (I32, [D, I32, I32, ctypes.POINTER(SZ)]),
@@ -92,6 +102,8 @@ def lib() -> ctypes.CDLL:
         "moe_graph_destroy": (I32, [P]),
         "moe_expert_ffn": (I32, [D, P, P, P, I32, S, P, P, P, P, P, P, SZ, P]),
         "moe_quantize_act": (I32, [D, P, P, P, P]),
+        "moe_linear_workspace_bytes": (I32, [LD, ctypes.POINTER(SZ)]),
+        "moe_linear": (I32, [LD, P, P, P, P, P, P, P, SZ, P]),
         "moe_strerror": (ctypes.c_char_p, [I32]),
         "moe_timing_enable": (I32, [I32]),
         "moe_timing_collect": (I32, [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(I64), I32]),
@@ -516,6 +528,85 @@ def moe_route_align(x: torch.Tensor, w_gate: torch.Tensor, top_k: int, *, interm
         _ptr(counts), _ptr(sorted_ids), _ptr(block_expert), _ptr(num_padded),
         ctypes.c_void_p(s.cuda_stream)))
     return logits, ids, w, counts, sorted_ids[:cap], block_expert[:cap // B], num_padded[:1], B
+
+
+_FNS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _rows(name: str, t: torch.Tensor, shape) -> int:
+    """The row stride of a matrix of the given shape whose rows are dense."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows, got strides {tuple(t.stride())}")
+    return t.stride(0) if rows > 1 else cols
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+               activation: Optional[str] = None, gated: bool = False,
+               scale: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """out [M, N] = act((x . w^T) * scale + bias) + residual, in x's dtype: the
+    dense product beside the experts.  x [M, K] and w [N, K] (or [2N, K] with
+    gated=True, gate rows first: act(gate) * up) in one of the layer's dtype
+    pairs; activation None, "relu", "silu", "gelu" or "gelu_tanh"; bias fp32
+    [rows of w]; scale fp32 [rows of w] or [1], for e4m3fn weights; residual
+    and out [M, N].  Rows may be longer in memory than K or N (views of wider
+    matrices).  out may be the residual."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [M, K] and w [rows, K]")
+    if activation not in _FNS:
+        raise ValueError(f"activation must be one of {list(_FNS)}, got {activation!r}")
+    M, K = x.shape
+    R = w.shape[0]
+    if gated and R % 2:
+        raise ValueError(f"a gated product needs an even number of weight rows, got {R}")
+    N = R // 2 if gated else R
+    act, wdt = _act_code(x), _w_code(w)
+    ldx, ldw = _rows("x", x, (M, K)), _rows("w", w, (R, K))
+    mode = MOE_SCALE_NONE
+    if wdt == MOE_DTYPE_E4M3FN:
+        if scale is None:
+            raise ValueError("e4m3fn weights need a scale")
+        if scale.dtype != torch.float32 or tuple(scale.shape) not in ((R,), (1,)):
+            raise ValueError(f"scale must be float32 [{R}] or [1]")
+        mode = MOE_SCALE_PER_CHANNEL if scale.shape[0] == R else MOE_SCALE_PER_TENSOR
+    elif scale is not None:
+        raise ValueError("scale is only for e4m3fn weights")
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (R,)):
+        raise ValueError(f"bias must be float32 [{R}]")
+    ldr = ldo = 0
+    if residual is not None:
+        if residual.dtype != x.dtype:
+            raise TypeError(f"residual must be {x.dtype}, got {residual.dtype}")
+        ldr = _rows("residual", residual, (M, N))
+    if out is not None:
+        if out.dtype != x.dtype:
+            raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+        ldo = _rows("out", out, (M, N))
+    dev = _dev(scale, bias)     # contiguous; the matrices only need dense rows
+    for t in (x, w, residual, out):
+        if t is not None:
+            if t.device.type != "cuda":
+                raise ValueError("all tensors must be on the GPU")
+            if dev is not None and t.device != dev:
+                raise ValueError("all tensors must be on one device")
+            dev = t.device
+    desc = moe_linear_desc(M, N, K, ldx, ldw, ldr, ldo, act, wdt, _FNS[activation],
+                           int(bool(gated)), mode, 0)
+    s = _launch_stream(dev, stream)
+    if out is None:
+        out = _alloc((M, N), x.dtype, dev, s)
+    n = ctypes.c_size_t()
+    _check("moe_linear_workspace_bytes",
+           lib().moe_linear_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)))
+    ws = _workspace(n.value, dev, workspace, s) if n.value else None
+    _check("moe_linear", lib().moe_linear(
+        ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(scale), _ptr(bias), _ptr(residual), _ptr(out),
+        _ptr(ws), n.value, ctypes.c_void_p(s.cuda_stream)))
+    return out
 
 
 class MoeGraph:

@@ -22,6 +22,7 @@ static __device__ __align__(256) unsigned char scratch[MOE_NOALLOC_WORKSPACE_BYT
 namespace {
 
 using moe::FfnArgs;
+using moe::LinearArgs;
 
 constexpr int64_t kMaxDim = int64_t(1) << 19;
 constexpr int64_t kMaxSlots = int64_t(1) << 30;
@@ -34,6 +35,11 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int act_bytes(int dt) { return dt == MOE_DTYPE_F32 ? 4 : 2; }
 
 // ------------------------------------------------------------ validation
+
+bool dtype_pair_ok(int act, int w) {
+  return (act == MOE_DTYPE_F32 && w == MOE_DTYPE_F32) ||
+         (act == MOE_DTYPE_BF16 && (w == MOE_DTYPE_BF16 || w == MOE_DTYPE_E4M3FN));
+}
 
 int check_desc(const moe_desc* d, int top_k) {
   if (!d) return MOE_ERR_NULL_PTR;
@@ -49,10 +55,7 @@ int check_desc(const moe_desc* d, int top_k) {
   if (d->num_experts < 1 || d->num_experts > moe::kMaxExperts) return MOE_ERR_BAD_SHAPE;
   if (top_k < 1 || top_k > d->num_experts || top_k > moe::kMaxTopK) return MOE_ERR_BAD_TOPK;
   if (d->num_tokens * top_k >= kMaxSlots) return MOE_ERR_BAD_SHAPE;
-  const bool pair_ok = (d->act_dtype == MOE_DTYPE_F32 && d->weight_dtype == MOE_DTYPE_F32) ||
-                       (d->act_dtype == MOE_DTYPE_BF16 && d->weight_dtype == MOE_DTYPE_BF16) ||
-                       (d->act_dtype == MOE_DTYPE_BF16 && d->weight_dtype == MOE_DTYPE_E4M3FN);
-  if (!pair_ok) return MOE_ERR_BAD_DTYPE;
+  if (!dtype_pair_ok(d->act_dtype, d->weight_dtype)) return MOE_ERR_BAD_DTYPE;
   const int bm = d->block_m;
   if (bm != 0 && bm != 16 && bm != 32 && bm != 64 && bm != 128 && bm != 256)
     return MOE_ERR_BAD_BLOCK_M;
@@ -852,6 +855,81 @@ MOE_API int moe_graph_destroy(moe_graph* graph) {
   const hipError_t e = graph->exec ? hipGraphExecDestroy(graph->exec) : hipSuccess;
   delete graph;
   return to_status(e);
+}
+
+// ------------------------------------------------------------ dense product
+
+constexpr int64_t kMaxLinearRows = int64_t(1) << 28;
+constexpr int64_t kMaxLinearDim = int64_t(1) << 20;
+constexpr int64_t kMaxLinearOut = int64_t(1) << 34;
+
+static int check_linear(const moe_linear_desc* d, LinearArgs* a) {
+  if (!d) return MOE_ERR_NULL_PTR;
+  if (d->reserved != 0 || (d->gated != 0 && d->gated != 1)) return MOE_ERR_BAD_ARG;
+  if (d->fn < MOE_FN_NONE || d->fn > MOE_FN_GELU_TANH) return MOE_ERR_BAD_ARG;
+  const int64_t M = d->rows, N = d->out_features, K = d->in_features;
+  if (M < 0 || M > kMaxLinearRows || N < 1 || N > kMaxLinearDim || K < 1 || K > kMaxLinearDim ||
+      M * N > kMaxLinearOut)
+    return MOE_ERR_BAD_SHAPE;
+  if (!dtype_pair_ok(d->act_dtype, d->weight_dtype)) return MOE_ERR_BAD_DTYPE;
+  const bool fp8 = d->weight_dtype == MOE_DTYPE_E4M3FN;
+  if (fp8 ? d->scale_mode != MOE_SCALE_PER_TENSOR && d->scale_mode != MOE_SCALE_PER_CHANNEL
+          : d->scale_mode != MOE_SCALE_NONE)
+    return MOE_ERR_BAD_DTYPE;
+  *a = LinearArgs{};
+  a->M = M;
+  a->N = static_cast<int>(N);
+  a->R = static_cast<int>(d->gated ? 2 * N : N);
+  a->K = static_cast<int>(K);
+  const int64_t len[4] = {K, K, N, N}, ld[4] = {d->ldx, d->ldw, d->ldr, d->ldo};
+  int64_t* to[4] = {&a->ldx, &a->ldw, &a->ldr, &a->ldo};
+  for (int i = 0; i < 4; ++i) {
+    if (ld[i] != 0 && (ld[i] < len[i] || ld[i] > kMaxLinearDim)) return MOE_ERR_BAD_SHAPE;
+    *to[i] = ld[i] ? ld[i] : len[i];
+  }
+  a->act_dtype = d->act_dtype;
+  a->w_dtype = d->weight_dtype;
+  a->fn = d->fn;
+  a->gated = d->gated != 0;
+  a->scale_channel = d->scale_mode == MOE_SCALE_PER_CHANNEL;
+  moe::linear_plan(a);
+  return MOE_OK;
+}
+
+MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* bytes) {
+  LinearArgs a;
+  const int st = check_linear(desc, &a);
+  if (st) return st;
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  *bytes = moe::linear_part_bytes(a);
+  return MOE_OK;
+}
+
+MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
+                       const float* scale, const float* bias, const void* residual, void* out,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  LinearArgs a;
+  int st = check_linear(desc, &a);
+  if (st) return st;
+  if (a.M == 0) return MOE_OK;
+  if ((st = check_ptrs({x, w, out}))) return st;
+  const bool scaled = desc->scale_mode != MOE_SCALE_NONE;
+  if (scaled && !scale) return MOE_ERR_NULL_PTR;
+  if (!scaled && scale) return MOE_ERR_BAD_DTYPE;
+  if (!aligned16(scale) || !aligned16(bias) || !aligned16(residual)) return MOE_ERR_MISALIGNED;
+  const size_t need = moe::linear_part_bytes(a);
+  if (need) {
+    if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return MOE_ERR_MISALIGNED;
+    a.part = static_cast<float*>(workspace);
+  }
+  a.x = x;
+  a.w = w;
+  a.scale = scale;
+  a.bias = bias;
+  a.res = residual;
+  a.out = out;
+  return to_status(moe::launch_linear(a, static_cast<hipStream_t>(stream)));
 }
 
 MOE_API int moe_timing_enable(int kind_mask) {

@@ -217,4 +217,35 @@ hipError_t launch_ffn_fused(const FfnArgs& a, hipStream_t s);
 // block estimate (the split length must be a multiple of it).
 int ffn2_kchunk(int d, int I, int B, int w_dtype, int act_dtype, int64_t blocks_est);
 
+// ------------------------------------------------------------ dense product
+
+// Mirrors of MOE_FN_* (moe.h).
+constexpr int kFnNone = 0;
+constexpr int kFnRelu = 1;
+constexpr int kFnSilu = 2;
+constexpr int kFnGelu = 3;
+constexpr int kFnGeluTanh = 4;
+
+struct LinearArgs {
+  const void* x;       // [M, K] act dtype
+  const void* w;       // [R, K] weight dtype
+  const float* scale;  // [R] or [1], or nullptr
+  const float* bias;   // [R] or nullptr
+  const void* res;     // [M, N] act dtype or nullptr
+  void* out;           // [M, N] act dtype
+  float* part;         // [splits, M, R] fp32 (workspace) when K is split, else nullptr
+  int64_t M;
+  int N, R, K;         // R = N, or 2N when gated
+  int64_t ldx, ldw, ldr, ldo;  // elements
+  int act_dtype, w_dtype, fn;
+  bool gated, scale_channel;
+  int splits;          // K ranges, each ksplit long (the last may be shorter)
+  int ksplit;
+};
+
+// Chooses the K split (the other fields set, pointers not yet needed).
+void linear_plan(LinearArgs* a);
+size_t linear_part_bytes(const LinearArgs& a);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+
 }  // namespace moe

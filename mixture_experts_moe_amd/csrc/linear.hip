@@ -1,0 +1,335 @@
+// Dense product with its epilogue: out = act((x . W^T) * scale + bias) +
+// residual, or act(gate half) * (up half) + residual when gated.  The kind
+// of product the routed experts run, without routing: shared experts, dense
+// feed-forward layers and projections beside a fused MoE layer.
+//
+// The product is computed transposed, as in the expert kernels: weight rows
+// (output channels) on the 16-row side of the MFMA and tokens on its columns,
+// so a lane ends with four consecutive channels of one token.
+
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+
+// ------------------------------------------------------------ epilogue
+//
+// Sums are fp32 throughout; the one rounding to the output type is the store
+// (to nearest even).  gelu through erfc and both sigmoids through
+// z / (1 + e^-u): no cancellation for large negative z, exp overflow gives a
+// quotient of zero.
+
+__device__ __forceinline__ float lin_act(int fn, float z) {
+  switch (fn) {
+    case kFnRelu: return z < 0.f ? 0.f : z;  // NaN stays
+    case kFnSilu: return silu(z);
+    case kFnGelu: return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case kFnGeluTanh:  // tanh(u) = 2 / (1 + e^-2u) - 1, u = sqrt(2/pi) (z + 0.044715 z^3)
+      return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+  }
+  return z;
+}
+
+// One output element from its channel sums (zu: the up half's, when gated).
+__device__ __forceinline__ float lin_value(const LinearArgs& a, float zg, float zu, int n) {
+  if (a.scale) {
+    zg *= a.scale_channel ? a.scale[n] : a.scale[0];
+    if (a.gated) zu *= a.scale_channel ? a.scale[a.N + n] : a.scale[0];
+  }
+  if (a.bias) {
+    zg += a.bias[n];
+    if (a.gated) zu += a.bias[a.N + n];
+  }
+  const float y = lin_act(a.fn, zg);
+  return a.gated ? y * zu : y;
+}
+
+template <typename AT>
+__device__ __forceinline__ float lin_load(const AT* p) {
+  if constexpr (sizeof(AT) == 4)
+    return *reinterpret_cast<const float*>(p);
+  else
+    return bf16_to_f32(*reinterpret_cast<const bf16_t*>(p));
+}
+
+template <typename AT>
+__device__ __forceinline__ void lin_store(AT* p, float v) {
+  if constexpr (sizeof(AT) == 4)
+    *p = v;
+  else
+    *p = f32_to_bf16(v);
+}
+
+// Finish and store out[m, n] (residual read and result written by one
+// thread, so out may be the residual itself).
+template <typename AT>
+__device__ __forceinline__ void lin_finish(const LinearArgs& a, float zg, float zu, int64_t m,
+                                           int n) {
+  float v = lin_value(a, zg, zu, n);
+  if (a.res) v += lin_load(static_cast<const AT*>(a.res) + m * a.ldr + n);
+  lin_store(static_cast<AT*>(a.out) + m * a.ldo + n, v);
+}
+
+// ------------------------------------------------------------ tiled product
+//
+// A workgroup computes TN weight rows x TM tokens, its waves in a WN x WM
+// grid of TA x TB 16x16 MFMA tiles each.  K moves through LDS in stages of
+// 128-byte rows (64 bf16 / 32 fp32; e4m3fn weights 64 bytes for the same 64
+// K) split into 16-byte units; unit s of row r sits in slot s ^ swz(r), so
+// that the 16 rows a 16-lane group reads for one s fall in 16 different
+// 16-byte bank groups.  Gated tiles hold TN/2 gate rows and the matching up
+// rows; a wave owns both of a channel.
+
+template <typename WT> struct LinTypes {
+  using AT = bf16_t;
+  static constexpr int kKC = 64;
+};
+template <> struct LinTypes<float> {
+  using AT = float;
+  static constexpr int kKC = 32;
+};
+
+template <typename WT, int WN_, int WM_, int TA_, int TB_>
+struct LinGeom {
+  using AT = typename LinTypes<WT>::AT;
+  static constexpr int WN = WN_, WM = WM_, TA = TA_, TB = TB_;
+  static constexpr int kThreads = 64 * WN * WM;
+  static constexpr int TN = 16 * TA * WN, TM = 16 * TB * WM;
+  static constexpr int kKC = LinTypes<WT>::kKC;            // K per stage
+  static constexpr int kWRow = kKC * (int)sizeof(WT);      // bytes of a weight row
+  static constexpr int kXRow = 128;                        // bytes of a token row
+  static constexpr int kWUnits = TN * kWRow / 16 / kThreads;  // 16-byte units per thread
+  static constexpr int kXUnits = TM * kXRow / 16 / kThreads;
+  static constexpr int kWBytes = TN * kWRow;
+  static constexpr int kStage = kWBytes + TM * kXRow;
+  static constexpr int kWRowsPerQ = kThreads / (kWRow / 16);
+  static constexpr int kXRowsPerQ = kThreads / (kXRow / 16);
+  static_assert(kWUnits >= 1 && kXUnits >= 1, "every thread loads");
+  static_assert(kWRowsPerQ % 16 == 0 && kXRowsPerQ % 16 == 0, "one swizzle per thread");
+};
+
+template <int kRowBytes>
+__device__ __forceinline__ int lin_swz(int row) {
+  return kRowBytes == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// A 16-byte unit of a row at any byte alignment of its element type.
+struct __attribute__((packed, aligned(1))) LinUnit {
+  uint4 v;
+};
+
+// Elements k .. k + 16/sizeof(T) - 1 of a row of K, zero past its end.
+template <typename T>
+__device__ __forceinline__ uint4 lin_unit(const T* row, int k, int K) {
+  constexpr int n = 16 / (int)sizeof(T);
+  if (k + n <= K) return reinterpret_cast<const LinUnit*>(row + k)->v;
+  union {
+    uint4 v;
+    T e[n];
+  } u;
+  u.v = uint4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    if (k + i < K) u.e[i] = row[k + i];
+  return u.v;
+}
+
+template <class G>
+using LinAcc = f32x4[G::TA][G::TB];
+
+// acc += W_rows . X_rows^T over one stage.  wrow(t), xrow(u): LDS rows of
+// this lane's 16-row tiles.
+template <typename WT, class G>
+__device__ __forceinline__ void lin_mma(const uint8_t* stage, const int (&wrow)[G::TA],
+                                        const int (&xrow)[G::TB], LinAcc<G>& acc) {
+  const uint8_t* ws = stage;
+  const uint8_t* xs = stage + G::kWBytes;
+  const int g = (threadIdx.x & 63) >> 4;
+  auto wunit = [&](int t, int s) {
+    return *reinterpret_cast<const uint4*>(ws + wrow[t] * G::kWRow +
+                                           ((s ^ lin_swz<G::kWRow>(wrow[t])) << 4));
+  };
+  auto xunit = [&](int u, int s) {
+    return *reinterpret_cast<const uint4*>(xs + xrow[u] * G::kXRow +
+                                           ((s ^ lin_swz<G::kXRow>(xrow[u])) << 4));
+  };
+  if constexpr (sizeof(WT) == 1) {
+    // a lane's 16 codes k = 16g .. 16g+15: the first eight in one MFMA, the
+    // last eight in the next, against the token units of the same k
+    uint4 x0[G::TB], x1[G::TB];
+#pragma unroll
+    for (int u = 0; u < G::TB; ++u) {
+      x0[u] = xunit(u, 2 * g);
+      x1[u] = xunit(u, 2 * g + 1);
+    }
+#pragma unroll
+    for (int t = 0; t < G::TA; ++t) {
+      const uint4 q = wunit(t, g);
+      const bf16x8 lo = as_frag(e4m3x8_to_frag_bits(q.x, q.y));
+      const bf16x8 hi = as_frag(e4m3x8_to_frag_bits(q.z, q.w));
+#pragma unroll
+      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(lo, as_frag(x0[u]), acc[t][u]);
+#pragma unroll
+      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(hi, as_frag(x1[u]), acc[t][u]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 wf[G::TA], xf[G::TB];
+#pragma unroll
+      for (int t = 0; t < G::TA; ++t) wf[t] = wunit(t, 4 * h + g);
+#pragma unroll
+      for (int u = 0; u < G::TB; ++u) xf[u] = xunit(u, 4 * h + g);
+      if constexpr (sizeof(WT) == 2) {
+#pragma unroll
+        for (int t = 0; t < G::TA; ++t)
+#pragma unroll
+          for (int u = 0; u < G::TB; ++u)
+            acc[t][u] = mfma16x16x32(as_frag(wf[t]), as_frag(xf[u]), acc[t][u]);
+      } else {
+        // MFMA i takes element i of every lane group's four k
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < G::TA; ++t)
+#pragma unroll
+            for (int u = 0; u < G::TB; ++u)
+              acc[t][u] = mfma16x16x4f32(__builtin_bit_cast(f32x4, wf[t])[i],
+                                         __builtin_bit_cast(f32x4, xf[u])[i], acc[t][u]);
+      }
+    }
+  }
+}
+
+// Tile row of wave row-index wn, tile t: gated waves hold gate tiles, then
+// the matching up tiles.
+template <class G, bool kGated>
+__device__ __forceinline__ int lin_tile_row(int wn, int t) {
+  if (!kGated) return 16 * (G::TA * wn + t);
+  constexpr int H = G::TA / 2;
+  return t < H ? 16 * (H * wn + t) : G::TN / 2 + 16 * (H * wn + t - H);
+}
+
+// Store the wave's tiles: finished outputs, or this K range's sums.
+template <typename WT, class G, bool kGated>
+__device__ __forceinline__ void lin_epilogue(const LinearArgs& a, LinAcc<G>& acc, int64_t m0,
+                                             int n0, int wn, int wm) {
+  using AT = typename G::AT;
+  const int lane = threadIdx.x & 63;
+  const int r16 = lane & 15, g = lane >> 4;
+  constexpr int H = kGated ? G::TA / 2 : G::TA;
+#pragma unroll
+  for (int u = 0; u < G::TB; ++u) {
+    const int64_t m = m0 + 16 * (G::TB * wm + u) + r16;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int t = 0; t < H; ++t) {
+      const int n = n0 + lin_tile_row<G, kGated>(wn, t) + 4 * g;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (n + v >= a.N) continue;
+        const float zg = acc[t][u][v];
+        const float zu = kGated ? acc[(t + H) % G::TA][u][v] : 0.f;
+        if (a.part) {
+          float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R;
+          p[n + v] = zg;
+          if (kGated) p[a.N + n + v] = zu;
+        } else {
+          lin_finish<AT>(a, zg, zu, m, n + v);
+        }
+      }
+    }
+  }
+}
+
+// Operands staged through registers: rows of any length and alignment.
+template <typename WT, class G, bool kGated>
+__global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a) {
+  using AT = typename G::AT;
+  __shared__ __attribute__((aligned(1024))) uint8_t stage[G::kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int gy = (a.N + (kGated ? G::TN / 2 : G::TN) - 1) / (kGated ? G::TN / 2 : G::TN);
+  const int n0 = (blockIdx.x % gy) * (kGated ? G::TN / 2 : G::TN);
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / gy) * G::TM;
+  const int k_begin = blockIdx.z * a.ksplit;
+  const int k_end = min(a.K, k_begin + a.ksplit);
+  const int wn = wave % G::WN, wm = wave / G::WN;
+
+  int wrow[G::TA], xrow[G::TB];
+#pragma unroll
+  for (int t = 0; t < G::TA; ++t) wrow[t] = lin_tile_row<G, kGated>(wn, t) + (lane & 15);
+#pragma unroll
+  for (int u = 0; u < G::TB; ++u) xrow[u] = 16 * (G::TB * wm + u) + (lane & 15);
+
+  LinAcc<G> acc;
+#pragma unroll
+  for (int t = 0; t < G::TA; ++t)
+#pragma unroll
+    for (int u = 0; u < G::TB; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const WT* w = static_cast<const WT*>(a.w);
+  const AT* x = static_cast<const AT*>(a.x);
+  for (int k0 = k_begin; k0 < k_end; k0 += G::kKC) {
+    uint4 wv[G::kWUnits], xv[G::kXUnits];
+#pragma unroll
+    for (int q = 0; q < G::kWUnits; ++q) {
+      const int tr = q * G::kWRowsPerQ + tid / (G::kWRow / 16);
+      const int k = k0 + ((tid % (G::kWRow / 16)) ^ lin_swz<G::kWRow>(tr)) * (16 / (int)sizeof(WT));
+      const int half = kGated && tr >= G::TN / 2;
+      const int n = n0 + tr - (half ? G::TN / 2 : 0);
+      wv[q] = n < a.N ? lin_unit<WT>(w + (static_cast<int64_t>(half) * a.N + n) * a.ldw, k, k_end)
+                      : uint4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int q = 0; q < G::kXUnits; ++q) {
+      const int tr = q * G::kXRowsPerQ + tid / 8;
+      const int k = k0 + ((tid % 8) ^ lin_swz<G::kXRow>(tr)) * (16 / (int)sizeof(AT));
+      xv[q] = m0 + tr < a.M ? lin_unit<AT>(x + (m0 + tr) * a.ldx, k, k_end) : uint4{0, 0, 0, 0};
+    }
+    __syncthreads();  // the previous stage has been read
+#pragma unroll
+    for (int q = 0; q < G::kWUnits; ++q)
+      *reinterpret_cast<uint4*>(stage + 16 * (q * G::kThreads + tid)) = wv[q];
+#pragma unroll
+    for (int q = 0; q < G::kXUnits; ++q)
+      *reinterpret_cast<uint4*>(stage + G::kWBytes + 16 * (q * G::kThreads + tid)) = xv[q];
+    __syncthreads();
+    lin_mma<WT, G>(stage, wrow, xrow, acc);
+  }
+  lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
+}
+
+// ------------------------------------------------------------ launchers
+
+template <typename WT, class G>
+static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
+  const int tn = a.gated ? G::TN / 2 : G::TN;
+  const dim3 grid(static_cast<unsigned>(((a.N + tn - 1) / tn) * ((a.M + G::TM - 1) / G::TM)), 1,
+                  a.splits);
+  if (a.gated)
+    linear_staged_kernel<WT, G, true><<<grid, G::kThreads, 0, s>>>(a);
+  else
+    linear_staged_kernel<WT, G, false><<<grid, G::kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+void linear_plan(LinearArgs* a) {
+  a->splits = 1;
+  a->ksplit = a->K;
+}
+
+size_t linear_part_bytes(const LinearArgs& a) {
+  return a.splits > 1 ? static_cast<size_t>(a.splits) * a.M * a.R * 4 : 0;
+}
+
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
+  switch (a.w_dtype) {
+    case kDtypeF32: return launch_staged<float, LinGeom<float, 2, 2, 2, 2>>(a, s);
+    case kDtypeBF16: return launch_staged<bf16_t, LinGeom<bf16_t, 2, 2, 2, 2>>(a, s);
+    case kDtypeE4M3FN: return launch_staged<fp8_t, LinGeom<fp8_t, 2, 2, 2, 2>>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe

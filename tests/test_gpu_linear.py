@@ -1,0 +1,218 @@
+"""moe_linear against the product in 64 bits.
+
+Tolerance.  A channel sum is a chain of fp32 MFMA accumulations, each wrong
+by at most one unit of 2^-23 of the running sum of magnitudes S = |x| . |w|^T
+(the matrix core may truncate); for bf16 and e4m3fn operands (exact products)
+an MFMA adds 16 or more k at once or four at a time, for fp32 one at a time
+with a rounded product, so at most n = K/4 + 64 (fp32: 2K + 64) errors of
+2^-23 S, plus one 2^-23 S each for the scale and the bias.  The activations
+have slopes of at most 1.13 (gated: the product rule), are themselves good to
+8 units of 2^-24, and the result is rounded once to the output type: half a
+step, eps/2 of its magnitude.
+"""
+
+import math
+
+import pytest
+import torch
+
+from mixture_experts_moe_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+FNS = [None, "relu", "silu", "gelu", "gelu_tanh"]
+FMTS = ["f32", "bf16", "e4m3fn"]
+
+
+def act64(z, fn):
+    if fn == "relu":
+        return z.clamp_min(0.0)
+    if fn == "silu":
+        return z * torch.sigmoid(z)
+    if fn == "gelu":
+        return z * torch.special.ndtr(z)
+    if fn == "gelu_tanh":
+        return 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+    return z
+
+
+def w64(w):
+    return w.view(torch.float8_e4m3fn).double() if w.dtype == torch.uint8 else w.double()
+
+
+def check(out, x, w, fn, gated, bias, scale, residual):
+    xd, wd = x.double(), w64(w)
+    K = x.shape[1]
+    z, S = xd @ wd.t(), xd.abs() @ wd.abs().t()
+    if scale is not None:
+        z, S = z * scale.double(), S * scale.double().abs()
+    if bias is not None:
+        z, S = z + bias.double(), S + bias.double().abs()
+    n = (2 * K if x.dtype == torch.float32 else K / 4) + 64
+    ez = n * 2.0 ** -23 * S
+    N = z.shape[1] // 2 if gated else z.shape[1]
+    y, ey = act64(z[:, :N], fn), 1.13 * ez[:, :N]
+    ey = ey + 8 * 2.0 ** -24 * y.abs()
+    if gated:
+        up, eu = z[:, N:], ez[:, N:]
+        ey = ey * up.abs() + (y.abs() + ey) * eu
+        y = y * up
+    if residual is not None:
+        y = y + residual.double()
+    tol = ey * (1 + 2.0 ** -8) + (torch.finfo(out.dtype).eps / 2 + 2.0 ** -22) * y.abs() + 1e-37
+    err = (out.double() - y).abs()
+    assert torch.isfinite(out.float()).all()
+    bad = err > tol
+    assert not bad.any(), (f"{int(bad.sum())} of {bad.numel()} outside: worst "
+                           f"{float((err / tol).max()):.3g} of the tolerance at "
+                           f"{bad.nonzero()[0].tolist()}")
+
+
+def inputs(M, N, K, fmt, gated=False, bias=True, residual=True, per_tensor=False, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(1000 * seed + M + 7 * N + 13 * K)
+    R = 2 * N if gated else N
+    adt = torch.float32 if fmt == "f32" else torch.bfloat16
+    x = torch.randn((M, K), generator=g, device="cuda").to(adt)
+    w = torch.randn((R, K), generator=g, device="cuda") * 0.1
+    scale = None
+    if fmt == "bf16":
+        w = w.to(torch.bfloat16)
+    elif fmt == "e4m3fn":
+        scale = (torch.rand((1 if per_tensor else R,), generator=g, device="cuda") + 0.5) * 0.1
+        w = (w * 10).to(torch.float8_e4m3fn).view(torch.uint8)
+    b = torch.randn((R,), generator=g, device="cuda") if bias else None
+    r = torch.randn((M, N), generator=g, device="cuda").to(adt) if residual else None
+    return x, w, b, scale, r
+
+
+SHAPES = [(1, 1, 1), (1, 5, 3), (2, 4, 64), (3, 64, 64), (5, 130, 520), (8, 256, 1024),
+          (16, 100, 256), (16, 1030, 2100), (17, 33, 65), (33, 512, 1024), (64, 64, 8),
+          (77, 1001, 777), (128, 128, 4096), (130, 260, 520), (257, 300, 64), (300, 515, 1000),
+          (512, 640, 320)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_values(M, N, K, gated, fmt):
+    print(f"linear {M}x{N}x{K} gated={gated} {fmt}", flush=True)
+    fn = FNS[(M + N + K) % len(FNS)]
+    x, w, b, scale, r = inputs(M, N, K, fmt, gated, bias=(N + K) % 3 > 0, residual=M % 2 > 0)
+    out = B.moe_linear(x, w, bias=b, activation=fn, gated=gated, scale=scale, residual=r)
+    check(out, x, w, fn, gated, b, scale, r)
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [4, 40])
+def test_each_activation_far_from_zero(M, gated, fn):
+    """Sums of up to about +-100: the tails of every activation."""
+    x, w, b, _, r = inputs(M, 48, 96, "f32", gated)
+    w = w * 30
+    out = B.moe_linear(x, w, bias=b, activation=fn, gated=gated, residual=r)
+    check(out, x, w, fn, gated, b, None, r)
+
+
+@pytest.mark.parametrize("M", [3, 80])
+def test_one_scale_for_the_whole_weight(M):
+    x, w, b, scale, r = inputs(M, 96, 256, "e4m3fn", per_tensor=True)
+    out = B.moe_linear(x, w, bias=b, scale=scale, residual=r)
+    check(out, x, w, None, False, b, scale, r)
+
+
+def padded(t, cols, fill):
+    """The same matrix as a view of rows `cols` elements longer."""
+    p = torch.full((t.shape[0], t.shape[1] + cols), fill, dtype=t.dtype, device=t.device)
+    p[:, :t.shape[1]] = t
+    return p, p[:, :t.shape[1]]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("pad", [1, 8, 64])
+@pytest.mark.parametrize("M,N,K", [(1, 48, 100), (7, 50, 72), (16, 300, 264), (70, 90, 136),
+                                   (300, 260, 328)])
+def test_rows_longer_than_their_length(M, N, K, pad, fmt):
+    """What lies between the rows (NaN here) is neither used nor written."""
+    print(f"linear strided {M}x{N}x{K} pad={pad} {fmt}", flush=True)
+    x, w, b, scale, r = inputs(M, N, K, fmt, True)
+    nan = float("nan")
+    _, xv = padded(x, pad, nan)
+    _, wv = padded(w, pad, 0x7F if fmt == "e4m3fn" else nan)
+    _, rv = padded(r, pad, nan)
+    buf = torch.full((M, N + pad), 7.0, dtype=x.dtype, device="cuda")
+    out = B.moe_linear(xv, wv, bias=b, activation="silu", gated=True, scale=scale, residual=rv,
+                       out=buf[:, :N])
+    assert out.data_ptr() == buf.data_ptr()
+    check(out, x, w, "silu", True, b, scale, r)
+    assert (buf[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 256), (5, 70, 130), (40, 256, 512), (290, 300, 256)])
+def test_bad_tokens_and_channels_stay_their_own(M, N, K):
+    """A NaN or infinite token, or weight row, reaches its own row or column only."""
+    x, w, b, _, _ = inputs(M, N, K, "bf16")
+    clean = B.moe_linear(x, w, bias=b)
+    x2, w2 = x.clone(), w.clone()
+    x2[M // 2, K - 1] = float("nan")
+    w2[N - 3, 0] = float("inf")
+    got = B.moe_linear(x2, w2, bias=b)
+    rows = [m for m in range(M) if m != M // 2]
+    cols = [n for n in range(N) if n != N - 3]
+    assert torch.isnan(got[M // 2]).all()
+    assert not torch.isfinite(got[:, N - 3]).any()
+    if rows:
+        assert torch.equal(got[rows][:, cols], clean[rows][:, cols])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(1, 128, 512), (9, 96, 3000), (48, 128, 4096), (200, 136, 640)])
+def test_out_may_be_the_residual(M, N, K, fmt):
+    x, w, b, scale, r = inputs(M, N, K, fmt)
+    want = B.moe_linear(x, w, bias=b, activation="gelu", scale=scale, residual=r)
+    r2 = r.clone()
+    got = B.moe_linear(x, w, bias=b, activation="gelu", scale=scale, residual=r2, out=r2)
+    assert got is r2 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 2048), (16, 640, 4096), (48, 256, 8192),
+                                   (300, 520, 1024)])
+def test_same_bits_every_time_and_in_a_graph(M, N, K):
+    x, w, b, _, r = inputs(M, N, K, "bf16")
+    want = B.moe_linear(x, w, bias=b, residual=r)
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        B.moe_linear(x, w, bias=b, residual=r, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_linear(x, w, bias=b, residual=r, out=out)
+    x1 = x.clone()
+    for i in range(3):
+        x.copy_(x1 * (i + 1))
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, B.moe_linear(x, w, bias=b, residual=r))
+
+
+def test_two_streams_with_their_own_workspaces():
+    a = inputs(48, 256, 8192, "bf16")
+    b = inputs(40, 512, 6144, "bf16")
+    want = [B.moe_linear(t[0], t[1], bias=t[2], residual=t[4]) for t in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i, t in enumerate((a, b)):
+            got[i].append(B.moe_linear(t[0], t[1], bias=t[2], residual=t[4], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_no_tokens():
+    x, w, b, _, r = inputs(4, 64, 64, "bf16")
+    assert B.moe_linear(x[:0], w, bias=b, residual=r[:0]).shape == (0, 64)
