@@ -303,6 +303,33 @@ MOE_API int moe_expert_ffn(const moe_desc* desc, const void* x, const void* w13,
 MOE_API int moe_quantize_act(const moe_desc* desc, const void* x, uint8_t* codes,
                              uint8_t* exps, void* stream);
 
+/* ---- the layer for a few tokens ---- */
+
+/* out = residual + MoE(x) for at most MOE_DECODE_MAX_TOKENS tokens, any dtype
+ * pair, expert count and top_k of the layer, in two launches: the router's
+ * logits, then selection, W13, SiLU * up, W2, gates and the sum over experts.
+ * The same layer as moe_forward (same router rule, h rounded to the act
+ * dtype; sums in another order, so equal within rounding), for the sizes
+ * where the number of launches and the tail of each are felt: moe_forward
+ * takes three to six there.  residual [T, d] (act dtype) may be NULL, or out
+ * itself; otherwise out overlaps no input.
+ *   - desc: block_m 0, act_quant MOE_ACT_AS_IS, T <= MOE_DECODE_MAX_TOKENS.
+ *   - schedule: between the two halves of the layer each workgroup needs the
+ *     others' part of h.  MOE_SCHED_AUTO waits for it, and computes a part
+ *     that stays missing for 2 ms itself (its owner may not have been
+ *     started, where other streams fill the GPU); MOE_SCHED_QUEUE computes a
+ *     missing part at once; MOE_SCHED_STATIC runs the halves as launches of
+ *     their own (three in all).  The bits are the same.
+ *   - workspace: moe_decode_workspace_bytes, 256-byte aligned; its contents
+ *     on entry do not matter.  Calls that may overlap need different ones.
+ * Deterministic; capturable into a graph; timed as route_logits and
+ * ffn_fused (moe_timing_enable). */
+#define MOE_DECODE_MAX_TOKENS 16
+MOE_API int moe_decode_workspace_bytes(const moe_desc* desc, int top_k, size_t* bytes);
+MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate, const void* w13,
+                       const void* w2, int top_k, const moe_scales* scales, const void* residual,
+                       void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- dense products beside the experts ---- */
 
 /* Activation of moe_linear's epilogue. */

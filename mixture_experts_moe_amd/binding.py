@@ -40,10 +40,11 @@ ENTRY_POINTS = (
     "moe_route_logits", "moe_align", "moe_route_align", "moe_expert_ffn",
     "moe_quantize_act", "moe_graph_create", "moe_graph_launch", "moe_graph_destroy", "moe_strerror",
     "moe_timing_enable", "moe_timing_collect", "moe_kernel_name", "moe_forward_noalloc",
-    "moe_linear_workspace_bytes", "moe_linear",
+    "moe_linear_workspace_bytes", "moe_linear", "moe_decode_workspace_bytes", "moe_decode",
 )
 MOE_ERR_NOALLOC_SIZE = -10
 MOE_NOALLOC_WORKSPACE_BYTES = 64 << 20
+MOE_DECODE_MAX_TOKENS = 16
 
 
 class moe_desc(ctypes.Structure):
@@ -102,6 +103,8 @@ def lib() -> ctypes.CDLL:
         "moe_graph_destroy": (I32, [P]),
         "moe_expert_ffn": (I32, [D, P, P, P, I32, S, P, P, P, P, P, P, SZ, P]),
         "moe_quantize_act": (I32, [D, P, P, P, P]),
+        "moe_decode_workspace_bytes": (I32, [D, I32, ctypes.POINTER(SZ)]),
+        "moe_decode": (I32, [D, P, P, P, P, I32, S, P, P, P, SZ, P]),
         "moe_linear_workspace_bytes": (I32, [LD, ctypes.POINTER(SZ)]),
         "moe_linear": (I32, [LD, P, P, P, P, P, P, P, SZ, P]),
         "moe_strerror": (ctypes.c_char_p, [I32]),
@@ -528,6 +531,43 @@ def moe_route_align(x: torch.Tensor, w_gate: torch.Tensor, top_k: int, *, interm
         _ptr(counts), _ptr(sorted_ids), _ptr(block_expert), _ptr(num_padded),
         ctypes.c_void_p(s.cuda_stream)))
     return logits, ids, w, counts, sorted_ids[:cap], block_expert[:cap // B], num_padded[:1], B
+
+
+def moe_decode_workspace_bytes(desc: moe_desc, top_k: int) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_decode_workspace_bytes",
+           lib().moe_decode_workspace_bytes(ctypes.byref(desc), int(top_k), ctypes.byref(n)))
+    return n.value
+
+
+def moe_decode(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+               top_k: int, scales: Optional[Sequence[torch.Tensor]] = None,
+               out: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None,
+               schedule: str = "auto") -> torch.Tensor:
+    """out [T, d] = residual + MoE(x) for at most MOE_DECODE_MAX_TOKENS tokens,
+    in two launches (moe_forward's layer; other arguments as there).
+    residual [T, d] in x's dtype, or None; out may be the residual."""
+    T, d, E, I = _shapes(x, w_gate, w13, w2)
+    if out is not None:
+        _check_out(out, x)
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError(f"residual must match x in shape and dtype: residual "
+                         f"{tuple(residual.shape)} {residual.dtype}, x {tuple(x.shape)} {x.dtype}")
+    dev = _dev(x, w_gate, w13, w2, residual, out)
+    desc = make_desc(T, d, E, I, _act_code(x), _w_code(w13), 0, None, schedule)
+    sc = _scales(w13, scales)
+    s = _launch_stream(dev, stream)
+    if out is None:
+        out = _alloc((T, d), x.dtype, dev, s)
+    nbytes = moe_decode_workspace_bytes(desc, top_k)
+    ws = _workspace(nbytes, dev, workspace, s)
+    st = lib().moe_decode(ctypes.byref(desc), _ptr(x), _ptr(w_gate), _ptr(w13), _ptr(w2),
+                          int(top_k), ctypes.byref(sc) if sc is not None else None,
+                          _ptr(residual), _ptr(out), _ptr(ws), nbytes,
+                          ctypes.c_void_p(s.cuda_stream))
+    _check("moe_decode", st)
+    return out
 
 
 _FNS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}

@@ -857,6 +857,110 @@ MOE_API int moe_graph_destroy(moe_graph* graph) {
   return to_status(e);
 }
 
+// ------------------------------------------------------------ few tokens
+
+// Ticks of the 100 MHz clock after which a workgroup computes a part of h
+// that is still missing: 2 ms, many times what the parts differ by.
+constexpr int64_t kDecodeWaitTicks = 200000;
+
+struct DecodePlan {
+  size_t logits, flags, h, total;
+};
+
+static int check_decode(const moe_desc* d, int top_k, DecodePlan* p) {
+  const int st = check_desc(d, top_k);
+  if (st) return st;
+  if (d->act_quant != MOE_ACT_AS_IS) return MOE_ERR_BAD_ARG;
+  if (d->block_m != 0) return MOE_ERR_BAD_BLOCK_M;
+  if (d->num_tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_BAD_SHAPE;
+  const size_t T = static_cast<size_t>(d->num_tokens);
+  p->logits = 0;
+  p->flags = round_up(T * d->num_experts * 4, kWsAlign);
+  p->h = p->flags + round_up(moe::decode_flag_bytes(), kWsAlign);
+  p->total = T ? p->h + round_up(T * top_k * d->intermediate * act_bytes(d->act_dtype), kWsAlign)
+               : 0;
+  return MOE_OK;
+}
+
+// Compute units of the device that runs `stream` (the current device for the
+// null stream).
+static int stream_cus(hipStream_t stream, int* cus) {
+  int dev = 0;
+  if (stream) {
+    hipDevice_t sd;
+    if (hipStreamGetDevice(stream, &sd) != hipSuccess) return MOE_ERR_HIP;
+    dev = static_cast<int>(sd);
+  } else if (hipGetDevice(&dev) != hipSuccess) {
+    return MOE_ERR_HIP;
+  }
+  if (hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+      *cus < 1)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+MOE_API int moe_decode_workspace_bytes(const moe_desc* desc, int top_k, size_t* bytes) {
+  DecodePlan p;
+  const int st = check_decode(desc, top_k, &p);
+  if (st) return st;
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  *bytes = p.total;
+  return MOE_OK;
+}
+
+MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate, const void* w13,
+                       const void* w2, int top_k, const moe_scales* scales, const void* residual,
+                       void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  DecodePlan p;
+  int st = check_decode(desc, top_k, &p);
+  if (st) return st;
+  if (desc->num_tokens == 0) return MOE_OK;
+  if ((st = check_scales(desc, scales))) return st;
+  if ((st = check_ptrs({x, w_gate, w13, w2, out}))) return st;
+  if (!aligned16(residual)) return MOE_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return MOE_ERR_MISALIGNED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int cus = 0;
+  if ((st = stream_cus(s, &cus))) return st;
+  char* ws = static_cast<char*>(workspace);
+  const bool fp8 = desc->weight_dtype == MOE_DTYPE_E4M3FN;
+  moe::DecodeArgs a{};
+  a.x = x;
+  a.w_gate = w_gate;
+  a.w13 = w13;
+  a.w2 = w2;
+  a.s13 = fp8 ? scales->w13 : nullptr;
+  a.s2 = fp8 ? scales->w2 : nullptr;
+  a.scale_mode = fp8 ? scales->mode : moe::kScaleNone;
+  a.w_dtype = desc->weight_dtype;
+  a.res = residual;
+  a.out = out;
+  a.logits = reinterpret_cast<float*>(ws + p.logits);
+  a.flags = reinterpret_cast<int32_t*>(ws + p.flags);
+  a.h = ws + p.h;
+  a.T = static_cast<int>(desc->num_tokens);
+  a.d = static_cast<int>(desc->hidden);
+  a.E = static_cast<int>(desc->num_experts);
+  a.I = static_cast<int>(desc->intermediate);
+  a.k = top_k;
+  a.wgs = moe::decode_workgroups(a.T, cus);
+  a.wait_limit = desc->schedule == MOE_SCHED_QUEUE ? 0 : kDecodeWaitTicks;
+  hipError_t e =
+      timed(MOE_KERNEL_ROUTE_LOGITS, s, [&] { return moe::launch_decode_route(a, s); });
+  auto layer = [&](int phases) {
+    if (e == hipSuccess)
+      e = timed(MOE_KERNEL_FFN_FUSED, s, [&] { return moe::launch_decode_layer(a, phases, s); });
+  };
+  if (desc->schedule == MOE_SCHED_STATIC) {
+    layer(1);
+    layer(2);
+  } else {
+    layer(3);
+  }
+  return to_status(e);
+}
+
 // ------------------------------------------------------------ dense product
 
 constexpr int64_t kMaxLinearRows = int64_t(1) << 28;

@@ -1,0 +1,593 @@
+// The whole MoE layer for at most 16 tokens in two launches.
+//
+//   1. decode_route_kernel: logits = x . W_gate^T (fp32), a workgroup per few
+//      experts; it also clears the flags below.
+//   2. decode_layer_kernel: every workgroup selects the experts from the
+//      logits by itself (a few hundred values, cheaper than another launch),
+//      computes its share of h = SiLU(W1 x) * (W3 x), publishes it, and then
+//      its share of the output channels: out = residual + sum_j gate_j W2 h_j,
+//      all experts of a channel in one workgroup, so nothing is added up
+//      through memory.
+//
+// With so few tokens the layer is a read of the selected experts' weights:
+// each is read exactly once (stream.h), whatever the number of its tokens.
+//
+// Between the two halves every workgroup needs every other's h.  Each
+// workgroup has a flag of its own, written once its h rows are out at device
+// scope, and reads all of them.  No workgroup depends on another one being
+// resident: one that finds a share missing for longer than the limit computes
+// that share itself (the same bits, to the same place), so every wait ends
+// whatever else the GPU runs.
+
+#include "kernels.h"
+#include "stream.h"
+
+namespace moe {
+
+constexpr int kDecThreads = 512;
+constexpr int kDecWaves = kDecThreads / 64;
+constexpr int kDecMaxRows = kDecodeMaxTokens * kMaxTopK;  // slots
+constexpr int kDecMaxWgs = 1024;
+
+// A value that every lane holds alike, as a scalar: addresses built from it
+// stay in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// ------------------------------------------------------------ router logits
+
+constexpr int kRouteThreads = 256;
+
+// EP experts per workgroup, TT >= T tokens; a thread takes every 256th unit
+// of four K.
+template <typename AT, int EP, int TT>
+__global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(
+    const AT* __restrict__ x, const float* __restrict__ w_gate, float* __restrict__ logits,
+    int32_t* __restrict__ flags, int nflags, int T, int E, int d) {
+  __shared__ float part[kRouteThreads / 64][EP * TT];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int e0 = blockIdx.x * EP;
+  if (blockIdx.x == 0)
+    for (int i = tid; i < nflags; i += kRouteThreads) flags[i] = 0;
+  float acc[EP][TT];
+#pragma unroll
+  for (int e = 0; e < EP; ++e)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[e][t] = 0.f;
+  for (int u = tid; u < d / 4; u += kRouteThreads) {
+    float4 w[EP];
+#pragma unroll
+    for (int e = 0; e < EP; ++e)
+      w[e] = *reinterpret_cast<const float4*>(
+          w_gate + static_cast<size_t>(min(e0 + e, E - 1)) * d + 4 * u);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      if (t < T) {
+        float v[4];
+        if constexpr (sizeof(AT) == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * d + 4 * u);
+          v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(x + static_cast<size_t>(t) * d + 4 * u);
+          v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+          v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
+        }
+#pragma unroll
+        for (int e = 0; e < EP; ++e) {
+          acc[e][t] = fmaf(w[e].x, v[0], acc[e][t]);
+          acc[e][t] = fmaf(w[e].y, v[1], acc[e][t]);
+          acc[e][t] = fmaf(w[e].z, v[2], acc[e][t]);
+          acc[e][t] = fmaf(w[e].w, v[3], acc[e][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EP; ++e)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float v = wave_sum(acc[e][t]);
+      if (lane == 0) part[wave][e * TT + t] = v;
+    }
+  __syncthreads();
+  if (tid < EP * TT) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRouteThreads / 64; ++w) v += part[w][tid];
+    const int e = e0 + tid / TT, t = tid % TT;
+    if (e < E && t < T) logits[static_cast<size_t>(t) * E + e] = v;
+  }
+}
+
+// ------------------------------------------------------------ selection
+
+// What the workgroup knows of the routing: the selected experts in index
+// order, each with its tokens in order.  A row is one (expert, token) pair;
+// expert i's rows are base[i] .. base[i+1]-1, and h has one row each.
+struct DecSel {
+  uint16_t expert[kMaxExperts];
+  uint16_t base[kMaxExperts + 1];
+  uint8_t token[kDecMaxRows];
+  float gate[kDecMaxRows];
+  uint16_t mask[kMaxExperts];  // tokens of each expert, while selecting
+  uint16_t slot_e[kDecMaxRows];
+  float slot_gate[kDecMaxRows];
+  int n;  // experts selected
+};
+
+// Order-preserving key: greater logit, greater key; NaN as -inf; both zeros
+// alike; 0 below every logit's key.
+__device__ __forceinline__ uint32_t dec_key(float v) {
+  if (v != v) v = -INFINITY;
+  if (v == 0.f) v = 0.f;
+  const uint32_t b = __float_as_uint(v);
+  return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float dec_logit(uint32_t key) {
+  return __uint_as_float((key >> 31) ? key & 0x7fffffffu : ~key);
+}
+
+// One wave selects the top k of a token's E logits: lane l holds experts
+// l*per .. l*per+per-1, so the first lane holding the maximum has the lowest
+// index; gates = softmax over the selection.
+__device__ __forceinline__ void dec_topk(const float* row, int E, int k, uint16_t* slot_e,
+                                         float* slot_gate) {
+  constexpr int kPer = kMaxExperts / 64;
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) >> 6;
+  uint32_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i < per) {  // uniform
+      const int e = lane * per + i;
+      const float v = row[min(e, E - 1)];
+      key[i] = e < E ? dec_key(v) : 0u;
+    } else {
+      key[i] = 0u;
+    }
+  uint32_t my_key = 0;
+  int my_e = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per && key[i] > best) {
+        best = key[i];
+        bi = i;
+      }
+    uint32_t m = best;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(m, off, 64)));
+    const int src = __ffsll(static_cast<unsigned long long>(__ballot(best == m))) - 1;
+    const int e = __shfl(lane * per + bi, src, 64);
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == bi) key[i] = 0;
+    }
+    if (lane == j) {
+      my_key = m;
+      my_e = e;
+    }
+  }
+  const float v = dec_logit(my_key);
+  const float l0 = __shfl(v, 0, 64);
+  const float p = lane < k ? expf(v - l0) : 0.f;
+  const float s = wave_sum(p);
+  if (lane < k) {
+    slot_e[lane] = static_cast<uint16_t>(my_e);
+    slot_gate[lane] = p / s;
+  }
+}
+
+__device__ __forceinline__ void dec_select(const float* logits, int T, int E, int k, DecSel& s) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int e = tid; e < E; e += kDecThreads) s.mask[e] = 0;
+  for (int t = wave; t < T; t += kDecWaves)
+    dec_topk(logits + static_cast<size_t>(t) * E, E, k, s.slot_e + t * k, s.slot_gate + t * k);
+  __syncthreads();
+  for (int f = tid; f < T * k; f += kDecThreads) {
+    const int e = s.slot_e[f];
+    // two 16-bit masks per word
+    atomicOr(reinterpret_cast<unsigned int*>(s.mask) + e / 2,
+             (1u << (f / k)) << (16 * (e & 1)));
+  }
+  __syncthreads();
+  if (wave == 0) {  // compact the used experts; rows in expert order
+    int n = 0, rows = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      const uint32_t m = e < E ? s.mask[e] : 0u;
+      const uint64_t used = __ballot(m != 0);
+      const int before = __popcll(used & ((1ull << lane) - 1));
+      const int cnt = __popc(m);
+      int incl = cnt;  // rows up to and with this lane's expert
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += o;
+      }
+      if (m) {
+        s.expert[n + before] = static_cast<uint16_t>(e);
+        s.base[n + before] = static_cast<uint16_t>(rows + incl - cnt);
+      }
+      n += __popcll(used);
+      rows += __shfl(incl, 63, 64);
+    }
+    if (lane == 0) {
+      s.base[n] = static_cast<uint16_t>(rows);
+      s.n = n;
+    }
+  }
+  __syncthreads();
+  // the row of each slot: its expert's position by binary search
+  const int n = s.n;
+  for (int f = tid; f < T * k; f += kDecThreads) {
+    const int e = s.slot_e[f], t = f / k;
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s.expert[mid] < e)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const int r = s.base[lo] + __popc(s.mask[e] & ((1u << t) - 1));
+    s.token[r] = static_cast<uint8_t>(t);
+    s.gate[r] = s.slot_gate[f];
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------ the layer
+
+
+template <typename WT, int TQ>
+struct DecLayer {
+  using G = StreamGeom<WT>;
+  using AT = typename G::AT;
+  const DecodeArgs& a;
+  DecSel& sel;
+  float (*red)[kDecodeMaxTokens][16];  // [2 * kDecWaves]: sums of 16 rows per token and wave
+
+  int lane, wave;
+
+  // Token rows of quad t of an expert with n rows from `base`; columns past
+  // the last repeat it (never stored).
+  template <int NQ, int RQ>
+  __device__ __forceinline__ void tokens(Stream<WT, RQ, NQ, true>& st, const AT* m, int ld,
+                                         int base, int n, bool h_rows) const {
+    const int unit = lane / 4 * (G::kLaneK * (int)sizeof(AT));
+    st.xb = reinterpret_cast<const uint8_t*>(m + (h_rows ? static_cast<size_t>(base) * ld : 0));
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int j = min(4 * t + (lane & 3), n - 1);
+      const int row = h_rows ? j : sel.token[base + j];
+      st.xo[t] = static_cast<uint32_t>(row) * ld * sizeof(AT) + unit;
+    }
+  }
+
+  // ---- W13: 8 channels (two gate quads, the matching up quads) from c0 of
+  // selected expert i, K split `sub` of `S`; sums to red[slot].
+  template <int NQ>
+  __device__ __forceinline__ void w13_group(int i, int c0, int sub, int S, int slot) const {
+    const int e = uniform(sel.expert[i]), base = uniform(sel.base[i]);
+    const int n = uniform(sel.base[i + 1]) - base;
+    Stream<WT, 4, NQ, true> st;
+    const size_t ldb = static_cast<size_t>(a.d) * sizeof(WT);
+    const uint8_t* w = static_cast<const uint8_t*>(a.w13) + static_cast<size_t>(e) * 2 * a.I * ldb;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      st.wq[q] = w + static_cast<size_t>((q >> 1) * a.I + c0 + 4 * (q & 1)) * ldb;
+      st.wo[q] = static_cast<uint32_t>((lane & 3) * ldb) + 16 * (lane >> 2);
+    }
+    tokens<NQ, 4>(st, static_cast<const AT*>(a.x), a.d, base, n, false);
+    f32x4 acc[4][NQ];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) acc[q][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int full = a.d / G::kChunk, left = a.d % G::kChunk;
+    const int mine = full > sub ? (full - sub + S - 1) / S : 0;
+    st.template run<NQ == 1 ? 4 : 2>(sub, mine, S, acc);
+    if (left && full % S == sub) st.tail(full, left, acc);
+#pragma unroll
+    for (int t = 0; t < NQ; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[q][t][v] = stream_wave_sum(acc[q][t][v]);
+        if (lane < 4) *reinterpret_cast<f32x4*>(&red[slot][4 * t + lane][4 * q]) = acc[q][t];
+      }
+  }
+
+  // K ranges per group so that the workgroup's waves finish together: the
+  // least time in chunks over S = 1, 2, 4, 8, counting about two chunks for
+  // a pass's start and end.
+  __device__ __forceinline__ int pick_split(int groups) const {
+    const int chunks = (a.d + G::kChunk - 1) / G::kChunk;
+    int best = 1 << 30, s = 1;
+    for (int S = 1; S <= kDecWaves; S *= 2) {
+      const int passes = (groups * S + kDecWaves - 1) / kDecWaves;
+      const int cost = passes * ((chunks + S - 1) / S + 2);
+      if (cost < best) {
+        best = cost;
+        s = S;
+      }
+    }
+    return s;
+  }
+
+  // Share b of h.
+  __device__ void w13_share(int b) const {
+    const int per = a.I / 8;  // groups per expert
+    const int64_t total = static_cast<int64_t>(uniform(sel.n)) * per;
+    const int g0 = static_cast<int>(total * b / a.wgs);
+    const int g1 = static_cast<int>(total * (b + 1) / a.wgs);
+    const int S = pick_split(g1 - g0);
+    const int at_once = kDecWaves / S;
+    const int sub = wave % S, gsel = wave / S;
+    int buf = 0;
+    for (int g = g0; g < g1; g += at_once, buf ^= kDecWaves) {
+      if (g + gsel < g1) {
+        const int i = (g + gsel) / per, c0 = 8 * ((g + gsel) % per);
+        const int n = uniform(sel.base[i + 1] - sel.base[i]);
+        if (TQ == 1 || n <= 4)
+          w13_group<1>(i, c0, sub, S, buf + wave);
+        else if (TQ == 2 || n <= 8)
+          w13_group<TQ >= 2 ? 2 : 1>(i, c0, sub, S, buf + wave);
+        else
+          w13_group<TQ>(i, c0, sub, S, buf + wave);
+      }
+      __syncthreads();
+      // channel pair cp of token column j of group gs
+      for (int o = threadIdx.x; o < at_once * 4 * TQ * 4; o += kDecThreads) {
+        const int cp = o & 3, j = (o >> 2) % (4 * TQ), gs = (o >> 2) / (4 * TQ);
+        if (g + gs >= g1) continue;
+        const int i = (g + gs) / per, c = 8 * ((g + gs) % per) + 2 * cp;
+        const int base = sel.base[i];
+        if (j >= sel.base[i + 1] - base) continue;
+        float hv[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          float zg = 0.f, zu = 0.f;
+          for (int s = 0; s < S; ++s) {
+            zg += red[buf + gs * S + s][j][2 * cp + v];
+            zu += red[buf + gs * S + s][j][8 + 2 * cp + v];
+          }
+          if (sizeof(WT) == 1) {
+            const size_t e = sel.expert[i];
+            const bool ch = a.scale_mode == kScaleChannel;
+            zg *= a.s13[ch ? e * 2 * a.I + c + v : e];
+            zu *= a.s13[ch ? e * 2 * a.I + a.I + c + v : e];
+          }
+          hv[v] = silu(zg) * zu;
+        }
+        // h is rounded to the activation type (the MFMA operand of W2), as
+        // the layer's other paths do; written at device scope for readers on
+        // other XCDs
+        AT* h = static_cast<AT*>(a.h) + static_cast<size_t>(base + j) * a.I + c;
+        if constexpr (sizeof(AT) == 2) {
+          const uint32_t v = f32_to_bf16(hv[0]) | (static_cast<uint32_t>(f32_to_bf16(hv[1])) << 16);
+          __hip_atomic_store(reinterpret_cast<uint32_t*>(h), v, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+          __hip_atomic_store(h, hv[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(h + 1, hv[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+    }
+  }
+
+  // ---- W2: output rows r0 .. r0+4*RQ-1.
+
+  // chunks [c0, c1) of selected expert i (the last may be partial); adds the
+  // expert's gated, scaled sums to the wave's out sums
+  template <int NQ, int RQ>
+  __device__ __forceinline__ void w2_part(int i, int r0, int c0, int c1) const {
+    const int e = uniform(sel.expert[i]), base = uniform(sel.base[i]);
+    const int n = uniform(sel.base[i + 1]) - base;
+    Stream<WT, RQ, NQ, true> st;
+    const size_t ldb = static_cast<size_t>(a.I) * sizeof(WT);
+    const uint8_t* w = static_cast<const uint8_t*>(a.w2) + (static_cast<size_t>(e) * a.d + r0) * ldb;
+#pragma unroll
+    for (int q = 0; q < RQ; ++q) {
+      st.wq[q] = w + 4 * q * ldb;
+      st.wo[q] = static_cast<uint32_t>((lane & 3) * ldb) + 16 * (lane >> 2);
+    }
+    tokens<NQ, RQ>(st, static_cast<const AT*>(a.h), a.I, base, n, true);
+    f32x4 acc[RQ][NQ];
+#pragma unroll
+    for (int q = 0; q < RQ; ++q)
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) acc[q][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int full = a.I / G::kChunk, left = a.I % G::kChunk;
+    st.template run<NQ == 1 ? 4 : 2>(c0, min(c1, full) - c0, 1, acc);
+    if (c1 > full) st.tail(full, left, acc);
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int j = 4 * t + (lane & 3);
+      const float gate = j < n ? sel.gate[base + j] : 0.f;
+#pragma unroll
+      for (int q = 0; q < RQ; ++q) {
+        f32x4 s;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          s[v] = stream_wave_sum(acc[q][t][v]);
+          if (sizeof(WT) == 1)
+            s[v] *= a.s2[a.scale_mode == kScaleChannel
+                             ? static_cast<size_t>(e) * a.d + r0 + 4 * q + v : e];
+        }
+        if (lane < 4 && j < n) {
+          float* o = &red[wave][sel.token[base + j]][4 * q];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] += gate * s[v];
+        }
+      }
+    }
+  }
+
+  template <int RQ>
+  __device__ __forceinline__ void w2_rows(int r0) const {
+    const int tid = threadIdx.x;
+    __syncthreads();  // the sums before have been read
+    for (int o = tid; o < kDecWaves * kDecodeMaxTokens * 16; o += kDecThreads)
+      (&red[0][0][0])[o] = 0.f;
+    __syncthreads();
+    // the waves share the (expert, chunk) list evenly
+    const int C = (a.I + G::kChunk - 1) / G::kChunk;
+    const int items = uniform(sel.n) * C;
+    const int i0 = items * wave / kDecWaves, i1 = items * (wave + 1) / kDecWaves;
+    for (int it = i0; it < i1;) {
+      const int i = it / C, c0 = it % C;
+      const int c1 = min(C, c0 + i1 - it);
+      const int n = uniform(sel.base[i + 1] - sel.base[i]);
+      if (TQ == 1 || n <= 4)
+        w2_part<1, RQ>(i, r0, c0, c1);
+      else if (TQ == 2 || n <= 8)
+        w2_part<TQ >= 2 ? 2 : 1, RQ>(i, r0, c0, c1);
+      else
+        w2_part<TQ, RQ>(i, r0, c0, c1);
+      it += c1 - c0;
+    }
+    __syncthreads();
+    for (int o = tid; o < a.T * 4 * RQ; o += kDecThreads) {
+      const int t = o / (4 * RQ), r = o % (4 * RQ);
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWaves; ++w) v += red[w][t][r];
+      const size_t at = static_cast<size_t>(t) * a.d + r0 + r;
+      if constexpr (sizeof(AT) == 2) {
+        if (a.res) v += bf16_to_f32(static_cast<const bf16_t*>(a.res)[at]);
+        static_cast<bf16_t*>(a.out)[at] = f32_to_bf16(v);
+      } else {
+        if (a.res) v += static_cast<const float*>(a.res)[at];
+        static_cast<float*>(a.out)[at] = v;
+      }
+    }
+  }
+
+  __device__ void w2_share(int b) const {
+    const int pairs = a.d / 8;  // of row quads
+    const int p1 = static_cast<int>(static_cast<int64_t>(pairs) * (b + 1) / a.wgs);
+    int p = static_cast<int>(static_cast<int64_t>(pairs) * b / a.wgs);
+    for (; p + 2 <= p1; p += 2) w2_rows<4>(8 * p);
+    if (p < p1) w2_rows<2>(8 * p);
+  }
+};
+
+// Share b is out (every thread's stores of it are complete before the barrier).
+__device__ __forceinline__ void dec_publish(int32_t* flags, int b) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) __hip_atomic_store(flags + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Waits until every share is out (-1), or until `limit` ticks of the 100 MHz
+// clock have passed: then one that is missing, the first from the caller's
+// own index on.
+__device__ __forceinline__ int dec_wait(const int32_t* flags, int wgs, int64_t limit, int* lds) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    const int64_t start = wall_clock64();
+    int found;
+    for (;;) {
+      int after = 1 << 30, any = 1 << 30;  // lowest missing index: from blockIdx on, of all
+      for (int i = lane; i < wgs; i += 64)
+        if (!__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) {
+          any = min(any, i);
+          if (i >= static_cast<int>(blockIdx.x)) after = min(after, i);
+        }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        any = min(any, __shfl_xor(any, off, 64));
+        after = min(after, __shfl_xor(after, off, 64));
+      }
+      found = __builtin_amdgcn_readfirstlane(after < (1 << 30) ? after : any);
+      if (found == 1 << 30 || wall_clock64() - start >= limit) break;
+      __builtin_amdgcn_s_sleep(2);
+    }
+    if (lane == 0) *lds = found == 1 << 30 ? -1 : found;
+  }
+  __syncthreads();
+  const int b = uniform(*lds);
+  __syncthreads();
+  return b;
+}
+
+template <typename WT, int TQ>
+__global__ __launch_bounds__(kDecThreads, TQ == 1 ? 4 : 2) void decode_layer_kernel(DecodeArgs a,
+                                                                                   int phases) {
+  __shared__ DecSel sel;
+  __shared__ __attribute__((aligned(16))) float red[2 * kDecWaves][kDecodeMaxTokens][16];
+  __shared__ int next;
+  dec_select(a.logits, a.T, a.E, a.k, sel);
+  const DecLayer<WT, TQ> layer{a, sel, red, static_cast<int>(threadIdx.x & 63),
+                               static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))};
+  if (phases & 1) {
+    int64_t limit = a.wait_limit;
+    for (int b = blockIdx.x; b >= 0; limit = 0) {  // b is wave-uniform
+      layer.w13_share(b);
+      if (!(phases & 2)) return;
+      dec_publish(a.flags, b);
+      b = dec_wait(a.flags, a.wgs, limit, &next);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // h as the others wrote it
+  }
+  layer.w2_share(blockIdx.x);
+}
+
+// ------------------------------------------------------------ launchers
+
+static int decode_quads(int T) { return T <= 4 ? 1 : T <= 8 ? 2 : 4; }
+
+int decode_workgroups(int T, int cus) {
+  const int n = decode_quads(T) == 1 ? 2 * cus : cus;  // as many as are resident at once
+  return n < kDecMaxWgs ? n : kDecMaxWgs;
+}
+
+size_t decode_flag_bytes() { return kDecMaxWgs * sizeof(int32_t); }
+
+template <typename AT, int TT>
+static void route(const DecodeArgs& a, hipStream_t s) {
+  constexpr int EP = 1;
+  decode_route_kernel<AT, EP, TT><<<(a.E + EP - 1) / EP, kRouteThreads, 0, s>>>(
+      static_cast<const AT*>(a.x), a.w_gate, a.logits, a.flags, a.wgs, a.T, a.E, a.d);
+}
+
+template <typename AT>
+static hipError_t route(const DecodeArgs& a, hipStream_t s) {
+  if (a.T <= 4)
+    route<AT, 4>(a, s);
+  else
+    route<AT, 16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s) {
+  return a.w_dtype == kDtypeF32 ? route<float>(a, s) : route<bf16_t>(a, s);
+}
+
+template <typename WT>
+static hipError_t layer(const DecodeArgs& a, int phases, hipStream_t s) {
+  switch (decode_quads(a.T)) {
+    case 1: decode_layer_kernel<WT, 1><<<a.wgs, kDecThreads, 0, s>>>(a, phases); break;
+    case 2: decode_layer_kernel<WT, 2><<<a.wgs, kDecThreads, 0, s>>>(a, phases); break;
+    default: decode_layer_kernel<WT, 4><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_decode_layer(const DecodeArgs& a, int phases, hipStream_t s) {
+  if (a.T < 1 || a.T > kDecodeMaxTokens || a.wgs < 1 || a.wgs > kDecMaxWgs)
+    return hipErrorInvalidValue;
+  switch (a.w_dtype) {
+    case kDtypeF32: return layer<float>(a, phases, s);
+    case kDtypeBF16: return layer<bf16_t>(a, phases, s);
+    case kDtypeE4M3FN: return layer<fp8_t>(a, phases, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe

@@ -248,4 +248,34 @@ void linear_plan(LinearArgs* a);
 size_t linear_part_bytes(const LinearArgs& a);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
+// ------------------------------------------------------------ few tokens
+
+constexpr int kDecodeMaxTokens = 16;
+
+struct DecodeArgs {
+  const void* x;        // [T, d]
+  const float* w_gate;  // [E, d]
+  const void* w13;      // [E, 2I, d]
+  const void* w2;       // [E, d, I]
+  const float* s13;     // scales or nullptr
+  const float* s2;
+  int scale_mode;
+  int w_dtype;
+  const void* res;      // [T, d] or nullptr
+  void* out;            // [T, d]
+  float* logits;        // [T, E] (workspace)
+  void* h;              // [T*k, I] act dtype (workspace)
+  int32_t* flags;       // decode_flag_bytes() (workspace), cleared by the route launch
+  int T, d, E, I, k;
+  int wgs;              // workgroups of the layer launch
+  int64_t wait_limit;   // 100 MHz ticks before a workgroup computes a missing share itself
+};
+
+// Workgroups that `cus` compute units hold at once, for T tokens.
+int decode_workgroups(int T, int cus);
+size_t decode_flag_bytes();
+hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s);
+// phases: 1 = W13, 2 = W2 and the sum over experts, 3 = both in one launch.
+hipError_t launch_decode_layer(const DecodeArgs& a, int phases, hipStream_t s);
+
 }  // namespace moe

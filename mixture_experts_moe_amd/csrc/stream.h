@@ -1,0 +1,224 @@
+// Weight streaming for a few tokens (at most 16): the matrix-vector end of a
+// product, bound by how fast the weight rows arrive.
+//
+// One load instruction takes four weight rows x 256 contiguous bytes: lane l
+// holds 16 bytes of row l % 4 at K unit l / 4.  The 4x4 MFMAs (16 independent
+// blocks of four lanes) take exactly that: block l / 4 multiplies its four
+// rows with four tokens over its own K unit, and the 16 blocks' sums are
+// added once at the end.  Against the 16x16 MFMA, whose operand layout makes
+// a load cover 16 rows x 64 bytes (half of each row's 128-byte line), this
+// reads whole lines with no LDS in between, for every weight type: 16 bytes
+// are 8 bf16 (two 4x4x4 MFMAs), 16 e4m3fn (widened to bf16 exactly, four) or
+// 4 fp32 (four 4x4x1).
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+typedef short bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename WT> struct StreamTypes {
+  using AT = bf16_t;
+};
+template <> struct StreamTypes<float> {
+  using AT = float;
+};
+
+template <typename WT>
+struct StreamGeom {
+  using AT = typename StreamTypes<WT>::AT;
+  static constexpr int kLaneK = 16 / (int)sizeof(WT);         // K per lane and load
+  static constexpr int kChunk = 16 * kLaneK;                  // K per load instruction
+  static constexpr int kTokLoads = kLaneK * (int)sizeof(AT) / 16;  // 16-byte loads per token
+};
+
+// D(4x4, f32) += A(4x4) . B(4x4) in each of 16 blocks: lane l supplies A row
+// and B column l % 4 of block l / 4 and receives D column l % 4, rows 0..3.
+__device__ __forceinline__ f32x4 mfma4x4x4(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
+                                           f32x4 c) {
+  const uint2 a{a0, a1}, b{b0, b1};
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(bf16x4, a),
+                                                __builtin_bit_cast(bf16x4, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma4x4x1(uint32_t a, uint32_t b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(a), __uint_as_float(b), c, 0, 0, 0);
+}
+
+// 16 bytes at any byte alignment.
+struct __attribute__((packed, aligned(1))) StreamUnit {
+  u32x4 v;
+};
+
+template <typename WT, int TQ>
+using StreamTok = u32x4[TQ][StreamGeom<WT>::kTokLoads];
+
+// acc[q][t] += rows of quad q . tokens of quad t over one chunk.
+template <typename WT, int RQ, int TQ>
+__device__ __forceinline__ void stream_mma(const u32x4 (&w)[RQ], const StreamTok<WT, TQ>& x,
+                                           f32x4 (&acc)[RQ][TQ]) {
+  if constexpr (sizeof(WT) == 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < TQ; ++t)
+#pragma unroll
+        for (int q = 0; q < RQ; ++q)
+          acc[q][t] = mfma4x4x4(w[q][2 * i], w[q][2 * i + 1], x[t][0][2 * i], x[t][0][2 * i + 1],
+                                acc[q][t]);
+  } else if constexpr (sizeof(WT) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < TQ; ++t)
+#pragma unroll
+        for (int q = 0; q < RQ; ++q) acc[q][t] = mfma4x4x1(w[q][i], x[t][0][i], acc[q][t]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // four codes of word i: K 4i .. 4i+3 of the lane's 16
+#pragma unroll
+      for (int q = 0; q < RQ; ++q) {
+        const uint32_t lo = e4m3x2_to_bf16x2(w[q][i], false), hi = e4m3x2_to_bf16x2(w[q][i], true);
+#pragma unroll
+        for (int t = 0; t < TQ; ++t)
+          acc[q][t] = mfma4x4x4(lo, hi, x[t][i / 2][2 * (i % 2)], x[t][i / 2][2 * (i % 2) + 1],
+                                acc[q][t]);
+      }
+    }
+  }
+}
+
+// The operand rows.  Weight quad q: wq[q] (wave-uniform) + wo[q] (this lane's
+// row and K unit, bytes); token quad t: xb (wave-uniform) + xo[t] (this
+// lane's token row and K unit).
+//
+// kAligned: every row starts at a multiple of 16 bytes; loads go through
+// buffer resources, and one whose `live` is false has a length of zero: it
+// returns zeros without a memory access, so the loops need no branches.  The
+// weights are read once: nontemporal.
+template <typename WT, int RQ, int TQ, bool kAligned>
+struct Stream {
+  using G = StreamGeom<WT>;
+  using AT = typename G::AT;
+  const uint8_t* wq[RQ];
+  uint32_t wo[RQ];
+  const uint8_t* xb;
+  uint32_t xo[TQ];
+
+  static constexpr int kWStep = 256;                            // bytes per chunk
+  static constexpr int kXStep = G::kChunk * (int)sizeof(AT);
+  static constexpr int kNonTemporal = 2;
+
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, bool live) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, live ? 0x7fffffff : 0,
+                                             0x00020000);
+  }
+
+  __device__ __forceinline__ void load(u32x4 (&w)[RQ], StreamTok<WT, TQ>& x, int chunk,
+                                       bool live) const {
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int q = 0; q < RQ; ++q)
+        w[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rsrc(wq[q], live), wo[q], chunk * kWStep,
+                                             kNonTemporal));
+#pragma unroll
+      for (int t = 0; t < TQ; ++t)
+#pragma unroll
+        for (int i = 0; i < G::kTokLoads; ++i)
+          x[t][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rsrc(xb, live), xo[t] + 16 * i, chunk * kXStep,
+                                                  0));
+    } else {
+#pragma unroll
+      for (int q = 0; q < RQ; ++q)
+        w[q] = reinterpret_cast<const StreamUnit*>(wq[q] + static_cast<size_t>(chunk) * kWStep +
+                                                   wo[q])
+                   ->v;
+#pragma unroll
+      for (int t = 0; t < TQ; ++t)
+#pragma unroll
+        for (int i = 0; i < G::kTokLoads; ++i)
+          x[t][i] = reinterpret_cast<const StreamUnit*>(
+                        xb + static_cast<size_t>(chunk) * kXStep + xo[t] + 16 * i)
+                        ->v;
+    }
+  }
+
+  // acc += over chunks c0, c0 + step, ... (n of them), P in flight.  Past the
+  // end a load is dead (aligned) or repeats the last chunk, unused.
+  template <int P>
+  __device__ __forceinline__ void run(int c0, int n, int step, f32x4 (&acc)[RQ][TQ]) const {
+    if (n <= 0) return;
+    u32x4 w[P][RQ];
+    StreamTok<WT, TQ> x[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) load(w[p], x[p], c0 + min(p, n - 1) * step, p < n);
+    for (int i = 0; i < n; i += P) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (kAligned || i + p < n) stream_mma<WT, RQ, TQ>(w[p], x[p], acc);
+        __builtin_amdgcn_sched_barrier(0);  // refill only what has been used: no second set
+        load(w[p], x[p], c0 + min(i + p + P, n - 1) * step, i + p + P < n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // The last, partial chunk: `left` (< kChunk) elements of K.
+  __device__ __forceinline__ void tail(int chunk, int left, f32x4 (&acc)[RQ][TQ]) const {
+    const int k = (threadIdx.x & 63) / 4 * G::kLaneK;  // this lane's K unit
+    u32x4 w[RQ];
+    StreamTok<WT, TQ> x;
+#pragma unroll
+    for (int q = 0; q < RQ; ++q)
+      w[q] = part<WT>(wq[q] + static_cast<size_t>(chunk) * kWStep + wo[q], left - k);
+#pragma unroll
+    for (int t = 0; t < TQ; ++t)
+#pragma unroll
+      for (int i = 0; i < G::kTokLoads; ++i)
+        x[t][i] = part<AT>(xb + static_cast<size_t>(chunk) * kXStep + xo[t] + 16 * i,
+                           left - k - i * (16 / (int)sizeof(AT)));
+    stream_mma<WT, RQ, TQ>(w, x, acc);
+  }
+
+  // 16 bytes of which the first n elements exist; zeros for the others.  With
+  // aligned rows whose length is a multiple of 16 bytes n is never in
+  // between.
+  template <typename T>
+  static __device__ __forceinline__ u32x4 part(const uint8_t* p, int n) {
+    constexpr int per = 16 / (int)sizeof(T);
+    union {
+      u32x4 v;
+      T e[per];
+    } u;
+    u.v = u32x4{0, 0, 0, 0};
+    if (n >= per) {
+      u.v = reinterpret_cast<const StreamUnit*>(p)->v;
+    } else if (!kAligned) {
+#pragma unroll
+      for (int i = 0; i < per; ++i)
+        if (i < n) u.e[i] = reinterpret_cast<const T*>(p)[i];
+    }
+    return u.v;
+  }
+};
+
+// Sum over the 16 blocks of a wave, four rows of 16 lanes first: afterwards
+// lane l holds its row of 16 lanes' sum for token l % 4.
+__device__ __forceinline__ float stream_row_sum(float v) {
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x124, 0xf,
+                                                          0xf, false));  // row_ror:4
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x128, 0xf,
+                                                          0xf, false));  // row_ror:8
+  return v;
+}
+__device__ __forceinline__ float stream_wave_sum(float v) {
+  v = stream_row_sum(v);
+  v += __shfl_xor(v, 16, kWave);
+  v += __shfl_xor(v, 32, kWave);
+  return v;
+}
+
+}  // namespace moe
