@@ -7,8 +7,8 @@
 // (output channels) on the 16-row side of the MFMA and tokens on its columns,
 // so a lane ends with four consecutive channels of one token.
 
-#include "common.h"
 #include "kernels.h"
+#include "stream.h"
 
 namespace moe {
 
@@ -300,7 +300,148 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
   lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
 }
 
+// ------------------------------------------------------------ few tokens
+//
+// At most 16 tokens: the product is a read of W (stream.h).  A workgroup
+// takes 16 * RT weight rows (gated: half of them gate rows, half the matching
+// up rows), its eight waves every eighth K chunk each, so that together they
+// read 2 KB of a row at a time; the waves' sums meet in LDS in a fixed order.
+
+constexpr int kLinStreamTokens = 16;
+constexpr int kLinStreamThreads = 512;
+constexpr int kLinStreamWaves = kLinStreamThreads / 64;
+
+// kQuads: at most four tokens, 4x4 MFMAs, else 16x16 (RT tiles of 16 rows;
+// gated: eight gate rows, then eight up rows).
+template <typename WT, int RT, bool kQuads, bool kGated, bool kAligned>
+__global__ __launch_bounds__(kLinStreamThreads, 4) void linear_stream_kernel(LinearArgs a) {
+  using G = StreamGeom<WT>;
+  using AT = typename G::AT;
+  using S16 = Stream16<WT, RT, kAligned>;
+  constexpr int kRows = 16 * RT, kCh = kGated ? kRows / 2 : kRows;
+  constexpr int kTok = kQuads ? 4 : 16, kParts = kQuads ? 4 * kLinStreamWaves : kLinStreamWaves;
+  // partial sums of four rows of a token; before them, the waves' weights
+  union Lds {
+    f32x4 red[kParts][kRows / 4][kTok];
+    uint8_t w[!kQuads && kAligned ? kLinStreamWaves : 1][S16::kLds];
+  };
+  __shared__ __attribute__((aligned(1024))) Lds lds;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * kCh;
+  const size_t ldb = a.ldw * sizeof(WT);
+  const int full = a.K / G::kChunk, left = a.K % G::kChunk;
+  const int mine = full > wave ? (full - wave + kLinStreamWaves - 1) / kLinStreamWaves : 0;
+  const bool last = left && full % kLinStreamWaves == wave;
+  const int M = static_cast<int>(a.M);
+  // The workgroup's channel c as a weight row, in its half of W; channels
+  // past the last repeat it (never stored).
+  auto first = [&](int c, bool up) {
+    return static_cast<const uint8_t*>(a.w) +
+           ((up ? static_cast<size_t>(a.N) : 0) + min(n0 + c, a.N - 1)) * ldb;
+  };
+  auto offset = [&](int c, int r) {  // from first(c) to row r after it
+    return static_cast<uint32_t>((min(n0 + c + r, a.N - 1) - min(n0 + c, a.N - 1)) * ldb);
+  };
+
+  if constexpr (kQuads) {
+    Stream<WT, 4 * RT, 1, kAligned> st;
+#pragma unroll
+    for (int q = 0; q < 4 * RT; ++q) {
+      const int c = 4 * q % kCh;
+      st.wq[q] = first(c, 4 * q >= kCh);
+      st.wo[q] = offset(c, lane & 3) + 16 * (lane >> 2);
+    }
+    st.xb = static_cast<const uint8_t*>(a.x);
+    st.xo[0] = static_cast<uint32_t>(min(lane & 3, M - 1) * a.ldx * sizeof(AT)) +
+               (lane >> 2) * (G::kLaneK * sizeof(AT));
+    f32x4 acc[4 * RT][1];
+#pragma unroll
+    for (int q = 0; q < 4 * RT; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.template run<4 / RT>(wave, mine, kLinStreamWaves, acc);
+    if (last) st.tail(full, left, acc);
+#pragma unroll
+    for (int q = 0; q < 4 * RT; ++q) {
+      f32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = stream_row_sum(acc[q][0][i]);
+      if ((lane & 12) == 0) lds.red[4 * wave + (lane >> 4)][q][lane & 3] = v;
+    }
+  } else {
+    S16 st;
+    auto row_off = [&](int t, int r) {
+      return kGated ? offset(8 * t, r & 7) : offset(16 * t + (r & 8), r & 7);
+    };
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      st.wq[t][0] = first(kGated ? 8 * t : 16 * t, false);
+      st.wq[t][1] = first(kGated ? 8 * t : 16 * t + 8, kGated);
+      st.place(t, [&](int r) { return row_off(t, r); });
+    }
+    st.lds = lds.w[!kQuads && kAligned ? wave : 0];
+    st.xb = static_cast<const uint8_t*>(a.x);
+    st.xo = static_cast<uint32_t>(min(lane & 15, M - 1) * a.ldx * sizeof(AT)) +
+            (lane >> 4) * (G::kLaneK * sizeof(AT));
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.run(wave, mine, kLinStreamWaves, acc);
+    if (last) st.tail(full, left, row_off, acc);
+    __syncthreads();  // the weights have been read
+#pragma unroll
+    for (int t = 0; t < RT; ++t) lds.red[wave][4 * t + (lane >> 4)][lane & 15] = acc[t];
+  }
+  __syncthreads();
+  for (int o = tid; o < kCh * kTok; o += kLinStreamThreads) {
+    const int c = o % kCh, m = o / kCh;
+    if (m >= M || n0 + c >= a.N) continue;
+    // the LDS rows of channel c (gate) and of its up row
+    const int rg = kGated && !kQuads ? c / 8 * 16 + c % 8 : c;
+    const int ru = kQuads ? (kCh + c) % kRows : (rg + 8) % kRows;
+    float zg = 0.f, zu = 0.f;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      zg += lds.red[p][rg / 4][m][rg % 4];
+      if (kGated) zu += lds.red[p][ru / 4][m][ru % 4];
+    }
+    lin_finish<AT>(a, zg, zu, m, n0 + c);
+  }
+}
+
 // ------------------------------------------------------------ launchers
+
+template <typename WT, int RT, bool kQuads, bool kGated>
+static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  constexpr int esz = 16 / (int)sizeof(WT), xsz = 16 / (int)sizeof(typename StreamGeom<WT>::AT);
+  const bool aligned = a.ldw % esz == 0 && a.ldx % xsz == 0 && a.K % esz == 0;
+  const int ch = kGated ? 8 * RT : 16 * RT;
+  const unsigned grid = static_cast<unsigned>((a.N + ch - 1) / ch);
+  if (aligned)
+    linear_stream_kernel<WT, RT, kQuads, kGated, true><<<grid, kLinStreamThreads, 0, s>>>(a);
+  else
+    linear_stream_kernel<WT, RT, kQuads, kGated, false><<<grid, kLinStreamThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename WT, bool kGated>
+static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  if (a.M <= 4) return launch_stream<WT, 1, true, kGated>(a, s);
+  // Tiles of weight rows that share each token load.  e4m3fn weights are half
+  // the bytes of their tokens, so more tiles pay as long as the grid still
+  // fills the chip: 16 x 14336 x 8192 44 us with one tile, 35 with two, 32
+  // with four; 16 x 4096 x 7168 11.3 and 13.3 us with one and two.
+  const int rt = sizeof(WT) > 1 || a.R < 6144 ? 1 : a.R < 12288 ? 2 : 4;
+  if constexpr (sizeof(WT) == 1) {
+    if (rt == 4) return launch_stream<WT, 4, false, kGated>(a, s);
+    if (rt == 2) return launch_stream<WT, 2, false, kGated>(a, s);
+  }
+  return launch_stream<WT, 1, false, kGated>(a, s);
+}
+
+template <typename WT>
+static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  return a.gated ? launch_stream<WT, true>(a, s) : launch_stream<WT, false>(a, s);
+}
 
 template <typename WT, class G>
 static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
@@ -324,6 +465,13 @@ size_t linear_part_bytes(const LinearArgs& a) {
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
+  if (a.M <= kLinStreamTokens) {
+    switch (a.w_dtype) {
+      case kDtypeF32: return launch_stream<float>(a, s);
+      case kDtypeBF16: return launch_stream<bf16_t>(a, s);
+      case kDtypeE4M3FN: return launch_stream<fp8_t>(a, s);
+    }
+  }
   switch (a.w_dtype) {
     case kDtypeF32: return launch_staged<float, LinGeom<float, 2, 2, 2, 2>>(a, s);
     case kDtypeBF16: return launch_staged<bf16_t, LinGeom<bf16_t, 2, 2, 2, 2>>(a, s);

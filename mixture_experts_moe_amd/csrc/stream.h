@@ -91,12 +91,11 @@ __device__ __forceinline__ void stream_mma(const u32x4 (&w)[RQ], const StreamTok
 
 // The operand rows.  Weight quad q: wq[q] (wave-uniform) + wo[q] (this lane's
 // row and K unit, bytes); token quad t: xb (wave-uniform) + xo[t] (this
-// lane's token row and K unit).
+// lane's token row and K unit; columns past the last token repeat it and are
+// dropped).
 //
-// kAligned: every row starts at a multiple of 16 bytes; loads go through
-// buffer resources, and one whose `live` is false has a length of zero: it
-// returns zeros without a memory access, so the loops need no branches.  The
-// weights are read once: nontemporal.
+// kAligned: every row starts at a multiple of 16 bytes.  The weights are read
+// once: nontemporal.
 template <typename WT, int RQ, int TQ, bool kAligned>
 struct Stream {
   using G = StreamGeom<WT>;
@@ -110,26 +109,24 @@ struct Stream {
   static constexpr int kXStep = G::kChunk * (int)sizeof(AT);
   static constexpr int kNonTemporal = 2;
 
-  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p, bool live) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, live ? 0x7fffffff : 0,
-                                             0x00020000);
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0x7fffffff, 0x00020000);
   }
 
-  __device__ __forceinline__ void load(u32x4 (&w)[RQ], StreamTok<WT, TQ>& x, int chunk,
-                                       bool live) const {
+  __device__ __forceinline__ void load(u32x4 (&w)[RQ], StreamTok<WT, TQ>& x, int chunk) const {
     if constexpr (kAligned) {
 #pragma unroll
       for (int q = 0; q < RQ; ++q)
-        w[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rsrc(wq[q], live), wo[q], chunk * kWStep,
-                                             kNonTemporal));
+        w[q] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(wq[q]), wo[q], chunk * kWStep,
+                                                         kNonTemporal));
 #pragma unroll
       for (int t = 0; t < TQ; ++t)
 #pragma unroll
         for (int i = 0; i < G::kTokLoads; ++i)
-          x[t][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rsrc(xb, live), xo[t] + 16 * i, chunk * kXStep,
-                                                  0));
+          x[t][i] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(xb), xo[t] + 16 * i,
+                                                           chunk * kXStep, 0));
     } else {
 #pragma unroll
       for (int q = 0; q < RQ; ++q)
@@ -146,24 +143,31 @@ struct Stream {
     }
   }
 
-  // acc += over chunks c0, c0 + step, ... (n of them), P in flight.  Past the
-  // end a load is dead (aligned) or repeats the last chunk, unused.
+  // N chunks from i on: all their loads, then their MFMAs.
+  template <int N>
+  __device__ __forceinline__ void batch(int c0, int step, f32x4 (&acc)[RQ][TQ]) const {
+    u32x4 w[N][RQ];
+    StreamTok<WT, TQ> x[N];
+#pragma unroll
+    for (int p = 0; p < N; ++p) load(w[p], x[p], c0 + p * step);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int p = 0; p < N; ++p) stream_mma<WT, RQ, TQ>(w[p], x[p], acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // acc += over chunks c0, c0 + step, ... (n of them), P at a time.  A wave
+  // waits for a whole batch; the other waves of its SIMD keep the loads
+  // coming (a ring that refills each chunk's registers as soon as they are
+  // used needs copies of the whole ring at its ends, which spill).
   template <int P>
   __device__ __forceinline__ void run(int c0, int n, int step, f32x4 (&acc)[RQ][TQ]) const {
-    if (n <= 0) return;
-    u32x4 w[P][RQ];
-    StreamTok<WT, TQ> x[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) load(w[p], x[p], c0 + min(p, n - 1) * step, p < n);
-    for (int i = 0; i < n; i += P) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (kAligned || i + p < n) stream_mma<WT, RQ, TQ>(w[p], x[p], acc);
-        __builtin_amdgcn_sched_barrier(0);  // refill only what has been used: no second set
-        load(w[p], x[p], c0 + min(i + p + P, n - 1) * step, i + p + P < n);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+    for (; n >= P; n -= P, c0 += P * step) batch<P>(c0, step, acc);
+    if (P > 2 && n >= 2) {
+      batch<2>(c0, step, acc);
+      n -= 2, c0 += 2 * step;
     }
+    if (n >= 1) batch<1>(c0, step, acc);
   }
 
   // The last, partial chunk: `left` (< kChunk) elements of K.
@@ -202,6 +206,164 @@ struct Stream {
         if (i < n) u.e[i] = reinterpret_cast<const T*>(p)[i];
     }
     return u.v;
+  }
+};
+
+// The same for 5 to 16 tokens on the 16x16 MFMAs: one token fragment serves
+// every tile of weight rows, where the 4x4 MFMAs need one per four tokens.
+// Their operand (lane l: row l % 16, K unit l / 16) would make a load cover 16
+// rows x 64 bytes, half lines, so aligned rows go through LDS: direct-to-LDS
+// loads of four rows x 256 bytes into the wave's own region, unit u of row r
+// in slot u ^ (r & 15) (the 16 rows read for one unit fall in 16 bank
+// groups).  acc[t]: D column (token) l % 16, rows 4 (l / 16) .. +3 of tile t,
+// already summed over K.
+// kHalf: the tiles have eight rows (the other eight sums mean nothing).
+template <typename WT, int RT, bool kAligned, bool kHalf = false>
+struct Stream16 {
+  using G = StreamGeom<WT>;
+  using AT = typename G::AT;
+  const uint8_t* wq[RT][2];  // wave-uniform: rows 0 and 8 of tile t
+  // this lane's byte offsets from those: aligned, of rows 4i + l / 16 for
+  // i = 0..3 with the unit that its LDS slot takes; else of row l % 16 at
+  // unit l / 16
+  uint32_t wo[RT][kAligned ? 4 : 1];
+  const uint8_t* xb;      // wave-uniform
+  uint32_t xo;            // this lane's token row and K unit, bytes
+  uint8_t* lds;           // the wave's kLds bytes (aligned)
+
+  static constexpr int kLds = RT * 4096;              // one chunk
+  static constexpr int kWStep = 256;
+  static constexpr int kXStep = G::kChunk * (int)sizeof(AT);
+  static constexpr int kUnits = 4;                    // MFMA operand units per row and chunk
+  static constexpr int kXUnit = kXStep / kUnits;      // token bytes a unit spans
+
+  using Toks = u32x4[kUnits][G::kTokLoads];
+
+  // The offsets of tile t: row_off(r) = bytes to row r from its half's base.
+  template <class F>
+  __device__ __forceinline__ void place(int t, F row_off) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        wo[t][i] = kHalf && i >= 2 ? 0 : row_off(r) + 16 * ((lane & 15) ^ r);
+      }
+    } else {
+      wo[t][0] = row_off(lane & (kHalf ? 7 : 15)) + 16 * (lane >> 4);
+    }
+  }
+
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const uint8_t* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, 0x7fffffff, 0x00020000);
+  }
+  // the base of this lane's row (l % 16) of tile t
+  __device__ __forceinline__ const uint8_t* lane_row(int t) const {
+    return !kHalf && (threadIdx.x & 8) ? wq[t][1] : wq[t][0];
+  }
+
+  __device__ __forceinline__ void load_x(Toks& x, int chunk) const {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+      for (int i = 0; i < G::kTokLoads; ++i)
+        if constexpr (kAligned)
+          x[u][i] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(xb), xo + kXUnit * u + 16 * i,
+                                                           chunk * kXStep, 0));
+        else
+          x[u][i] = reinterpret_cast<const StreamUnit*>(xb + static_cast<size_t>(chunk) * kXStep +
+                                                        xo + kXUnit * u + 16 * i)
+                        ->v;
+  }
+
+  static __device__ __forceinline__ f32x4 mma(u32x4 w, const u32x4 (&x)[G::kTokLoads], f32x4 acc) {
+    if constexpr (sizeof(WT) == 2) {
+      return mfma16x16x32(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x[0]), acc);
+    } else if constexpr (sizeof(WT) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = mfma16x16x4f32(__uint_as_float(w[i]), __uint_as_float(x[0][i]), acc);
+      return acc;
+    } else {
+      acc = mfma16x16x32(as_frag(e4m3x8_to_frag_bits(w[0], w[1])),
+                         __builtin_bit_cast(bf16x8, x[0]), acc);
+      return mfma16x16x32(as_frag(e4m3x8_to_frag_bits(w[2], w[3])),
+                          __builtin_bit_cast(bf16x8, x[G::kTokLoads - 1]), acc);
+    }
+  }
+
+  __device__ __forceinline__ void chunk(int c, f32x4 (&acc)[RT]) const {
+    Toks x;
+    if constexpr (kAligned) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < (kHalf ? 2 : 4); ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rsrc(wq[t][i / 2]), (__attribute__((address_space(3))) void*)(lds + 4096 * t + 1024 * i), 16,
+              wo[t][i], c * kWStep, 0, 2);
+      load_x(x, c);
+      // the loads have landed; the compiler does not see that the LDS reads
+      // below depend on them
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const int r16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          acc[t] = mma(*reinterpret_cast<const u32x4*>(lds + 4096 * t + 256 * r16 +
+                                                       16 * ((4 * u + g) ^ r16)),
+                       x[u], acc[t]);
+      // every read has returned before the next chunk's loads overwrite them
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    } else {
+      u32x4 w[kUnits][RT];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          w[u][t] = reinterpret_cast<const StreamUnit*>(
+                        lane_row(t) + static_cast<size_t>(c) * kWStep + wo[t][0] + 64 * u)
+                        ->v;
+      load_x(x, c);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] = mma(w[u][t], x[u], acc[t]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  // acc += over chunks c0, c0 + step, ... (n of them), one at a time per wave.
+  __device__ __forceinline__ void run(int c0, int n, int step, f32x4 (&acc)[RT]) const {
+    for (; n >= 1; --n, c0 += step) chunk(c0, acc);
+  }
+
+  // The last, partial chunk: `left` (< kChunk) elements of K; row_off as for
+  // place().
+  template <class F>
+  __device__ __forceinline__ void tail(int c, int left, F row_off, f32x4 (&acc)[RT]) const {
+    using S = Stream<WT, 1, 1, kAligned>;
+    constexpr int per = 16 / (int)sizeof(AT);
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int k = (4 * u + (lane >> 4)) * G::kLaneK;
+      u32x4 x[G::kTokLoads];
+#pragma unroll
+      for (int i = 0; i < G::kTokLoads; ++i)
+        x[i] = S::template part<AT>(
+            xb + static_cast<size_t>(c) * kXStep + xo + kXUnit * u + 16 * i, left - k - i * per);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        acc[t] = mma(S::template part<WT>(lane_row(t) + static_cast<size_t>(c) * kWStep +
+                                              row_off(t, lane & (kHalf ? 7 : 15)) +
+                                              16 * (lane >> 4) + 64 * u,
+                                          left - k),
+                     x, acc[t]);
+    }
   }
 };
 
