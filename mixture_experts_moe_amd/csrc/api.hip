@@ -996,6 +996,7 @@ static int check_linear(const moe_linear_desc* d, LinearArgs* a) {
   a->fn = d->fn;
   a->gated = d->gated != 0;
   a->scale_channel = d->scale_mode == MOE_SCALE_PER_CHANNEL;
+  a->vec4 = a->ldo % 4 == 0 && a->ldr % 4 == 0;  // the buffers are 16-byte aligned
   moe::linear_plan(a);
   return MOE_OK;
 }

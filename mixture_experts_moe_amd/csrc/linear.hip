@@ -70,6 +70,51 @@ __device__ __forceinline__ void lin_finish(const LinearArgs& a, float zg, float 
   lin_store(static_cast<AT*>(a.out) + m * a.ldo + n, v);
 }
 
+// Four consecutive channels n .. n+3 of token m (those below N): finished
+// outputs, or this K range's sums where K is split.
+template <typename AT, bool kGated>
+__device__ __forceinline__ void lin_store4(const LinearArgs& a, f32x4 zg, f32x4 zu, int64_t m,
+                                           int n) {
+  if (a.part) {
+    float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (n + v < a.N) {
+        p[n + v] = zg[v];
+        if (kGated) p[a.N + n + v] = zu[v];
+      }
+    return;
+  }
+  if (a.vec4 && n + 4 <= a.N) {  // rows and residual rows in whole vectors
+    AT* o = static_cast<AT*>(a.out) + m * a.ldo + n;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lin_value(a, zg[i], kGated ? zu[i] : 0.f, n + i);
+    if constexpr (sizeof(AT) == 4) {
+      if (a.res) {
+        const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.res) +
+                                                          m * a.ldr + n);
+        v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
+      }
+      *reinterpret_cast<float4*>(o) = float4{v[0], v[1], v[2], v[3]};
+    } else {
+      if (a.res) {
+        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const bf16_t*>(a.res) +
+                                                        m * a.ldr + n);
+        v[0] += __uint_as_float(r.x << 16), v[1] += __uint_as_float(r.x & 0xffff0000u);
+        v[2] += __uint_as_float(r.y << 16), v[3] += __uint_as_float(r.y & 0xffff0000u);
+      }
+      *reinterpret_cast<uint2*>(o) =
+          uint2{f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
+                f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16)};
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (n + v < a.N) lin_finish<AT>(a, zg[v], kGated ? zu[v] : 0.f, m, n + v);
+}
+
 // ------------------------------------------------------------ tiled product
 //
 // A workgroup computes TN weight rows x TM tokens, its waves in a WN x WM
@@ -114,20 +159,18 @@ __device__ __forceinline__ int lin_swz(int row) {
 }
 
 // A 16-byte unit of a row at any byte alignment of its element type.
-struct __attribute__((packed, aligned(1))) LinUnit {
-  uint4 v;
-};
+typedef StreamUnit LinUnit;
 
 // Elements k .. k + 16/sizeof(T) - 1 of a row of K, zero past its end.
 template <typename T>
-__device__ __forceinline__ uint4 lin_unit(const T* row, int k, int K) {
+__device__ __forceinline__ u32x4 lin_unit(const T* row, int k, int K) {
   constexpr int n = 16 / (int)sizeof(T);
   if (k + n <= K) return reinterpret_cast<const LinUnit*>(row + k)->v;
   union {
-    uint4 v;
+    u32x4 v;
     T e[n];
   } u;
-  u.v = uint4{0, 0, 0, 0};
+  u.v = u32x4{0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < n; ++i)
     if (k + i < K) u.e[i] = row[k + i];
@@ -225,19 +268,7 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs& a, LinAcc<G>& acc
 #pragma unroll
     for (int t = 0; t < H; ++t) {
       const int n = n0 + lin_tile_row<G, kGated>(wn, t) + 4 * g;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (n + v >= a.N) continue;
-        const float zg = acc[t][u][v];
-        const float zu = kGated ? acc[(t + H) % G::TA][u][v] : 0.f;
-        if (a.part) {
-          float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R;
-          p[n + v] = zg;
-          if (kGated) p[a.N + n + v] = zu;
-        } else {
-          lin_finish<AT>(a, zg, zu, m, n + v);
-        }
-      }
+      lin_store4<AT, kGated>(a, acc[t][u], acc[(t + H) % G::TA][u], m, n);
     }
   }
 }
@@ -271,7 +302,7 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
   const WT* w = static_cast<const WT*>(a.w);
   const AT* x = static_cast<const AT*>(a.x);
   for (int k0 = k_begin; k0 < k_end; k0 += G::kKC) {
-    uint4 wv[G::kWUnits], xv[G::kXUnits];
+    u32x4 wv[G::kWUnits], xv[G::kXUnits];
 #pragma unroll
     for (int q = 0; q < G::kWUnits; ++q) {
       const int tr = q * G::kWRowsPerQ + tid / (G::kWRow / 16);
@@ -279,25 +310,357 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
       const int half = kGated && tr >= G::TN / 2;
       const int n = n0 + tr - (half ? G::TN / 2 : 0);
       wv[q] = n < a.N ? lin_unit<WT>(w + (static_cast<int64_t>(half) * a.N + n) * a.ldw, k, k_end)
-                      : uint4{0, 0, 0, 0};
+                      : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int q = 0; q < G::kXUnits; ++q) {
       const int tr = q * G::kXRowsPerQ + tid / 8;
       const int k = k0 + ((tid % 8) ^ lin_swz<G::kXRow>(tr)) * (16 / (int)sizeof(AT));
-      xv[q] = m0 + tr < a.M ? lin_unit<AT>(x + (m0 + tr) * a.ldx, k, k_end) : uint4{0, 0, 0, 0};
+      xv[q] = m0 + tr < a.M ? lin_unit<AT>(x + (m0 + tr) * a.ldx, k, k_end) : u32x4{0, 0, 0, 0};
     }
     __syncthreads();  // the previous stage has been read
 #pragma unroll
     for (int q = 0; q < G::kWUnits; ++q)
-      *reinterpret_cast<uint4*>(stage + 16 * (q * G::kThreads + tid)) = wv[q];
+      *reinterpret_cast<u32x4*>(stage + 16 * (q * G::kThreads + tid)) = wv[q];
 #pragma unroll
     for (int q = 0; q < G::kXUnits; ++q)
-      *reinterpret_cast<uint4*>(stage + G::kWBytes + 16 * (q * G::kThreads + tid)) = xv[q];
+      *reinterpret_cast<u32x4*>(stage + G::kWBytes + 16 * (q * G::kThreads + tid)) = xv[q];
     __syncthreads();
     lin_mma<WT, G>(stage, wrow, xrow, acc);
   }
   lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
+}
+
+// ------------------------------------------------------------ large products
+//
+// 256 weight rows x 256 tokens per workgroup, eight waves of 128 x 64 (two
+// per SIMD), each wave's tile in four quadrants of 64 x 32.  A K stage of
+// 128-byte rows is four pieces of 128 rows (the rows of quadrant row 0 and 1,
+// the tokens of quadrant column 0 and 1; gated: gate rows and up rows), each
+// in an LDS array of its own, two buffers.  A stage runs in four phases, one
+// per quadrant:
+//   load part:    the phase's new fragments LDS -> registers; the direct-to-
+//                 LDS loads of one or two pieces of the next stage; a wait for
+//                 the piece that the next phase reads
+//   matrix part:  the quadrant's MFMAs
+// with a workgroup barrier after each part.  The waves of one half of the
+// workgroup run one barrier behind the others: on every SIMD one wave's
+// MFMAs run while the other loads, with the matrix wave's priority raised.
+// A piece is loaded three to four phases (about a microsecond) before it is
+// read.  Rows past M or N and K past the end read from past the end of their
+// buffer resource: zeros, without a memory access.
+
+constexpr int kPpThreads = 512;
+constexpr int kPpPiece = 128;  // rows of a piece
+constexpr uint32_t kPpDead = 0x80000000u;  // an offset past every resource
+
+__device__ __forceinline__ void pp_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+template <int N>
+__device__ __forceinline__ void pp_wait_loads() {
+  static_assert(N >= 0 && N <= 63, "six-bit count");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// 16 bytes per lane from a resource straight into LDS (64 lanes: 1 KB from
+// `lds`).
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off,
+                                           int base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off,
+                                           base, 0, 0);
+}
+
+// One operand's direct-to-LDS loads: piece p holds rows 128p .. 128p+127 of
+// the tile.
+template <typename T, int kRowBytes>
+struct PpLoader {
+  static constexpr int kUnits = kRowBytes / 16;                       // per row
+  static constexpr int kLoads = kPpPiece * kUnits / kPpThreads;       // per piece and thread
+  static constexpr int kStep = kPpThreads / kUnits;                   // rows between loads
+  static_assert(kLoads >= 1, "every thread loads");
+  __amdgpu_buffer_rsrc_t r[2];
+  uint32_t off[kLoads];
+  int ke;  // this lane's K within a stage
+
+  // base*: the pieces' first rows; rows*: their rows that exist (others lie
+  // past the resource's end); K in elements
+  __device__ __forceinline__ void init(const uint8_t* base0, const uint8_t* base1, int64_t rows0,
+                                       int64_t rows1, int64_t ld, int K) {
+    const int tid = threadIdx.x;
+    const int row = tid / kUnits;
+    ke = ((tid % kUnits) ^ lin_swz<kRowBytes>(row)) * (16 / (int)sizeof(T));
+    r[0] = resource(base0, rows0, ld, K);
+    r[1] = resource(base1, rows1, ld, K);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      off[q] = static_cast<uint32_t>((row + q * kStep) * ld + ke) * (uint32_t)sizeof(T);
+  }
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base,
+                                                                    int64_t rows, int64_t ld,
+                                                                    int K) {
+    const int64_t n = rows < kPpPiece ? rows : kPpPiece;
+    const int64_t bytes = n > 0 ? ((n - 1) * ld + K) * (int)sizeof(T) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                             static_cast<int>(bytes), 0x00020000);
+  }
+  // K k0 .. of piece p into lds
+  __device__ __forceinline__ void issue(int p, uint8_t* lds, int k0, int k_end) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      lds_load16(r[p], lds + (q * kPpThreads + 64 * wave) * 16,
+                 k0 + ke < k_end ? off[q] : kPpDead, k0 * (int)sizeof(T));
+  }
+};
+
+template <typename WT>
+struct PpTypes {
+  using AT = typename LinTypes<WT>::AT;
+  static constexpr int kKC = LinTypes<WT>::kKC;
+  static constexpr int kWRow = kKC * (int)sizeof(WT);
+  static constexpr int kWFrags = kWRow / 64;  // 16-byte reads per row and stage
+  static constexpr int kW = 4, kX = 2;        // 16-row tiles of a quadrant
+};
+
+template <typename WT>
+struct PpFrags {
+  using P = PpTypes<WT>;
+  u32x4 w[P::kW][P::kWFrags];
+  u32x4 x[2][P::kX][2];  // both quadrant columns
+};
+
+template <typename WT>
+__device__ __forceinline__ void pp_read_w(PpFrags<WT>& f, const uint8_t* piece, int row0) {
+  using P = PpTypes<WT>;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int t = 0; t < P::kW; ++t) {
+    const int row = row0 + 16 * t + (lane & 15);
+#pragma unroll
+    for (int h = 0; h < P::kWFrags; ++h)
+      f.w[t][h] = *reinterpret_cast<const u32x4*>(
+          piece + row * P::kWRow + (((4 * h + (lane >> 4)) ^ lin_swz<P::kWRow>(row)) << 4));
+  }
+}
+template <typename WT>
+__device__ __forceinline__ void pp_read_x(PpFrags<WT>& f, int j, const uint8_t* piece, int row0) {
+  using P = PpTypes<WT>;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < P::kX; ++u) {
+    const int row = row0 + 16 * u + (lane & 15);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int slot = sizeof(WT) == 1 ? 2 * g + h : 4 * h + g;
+      f.x[j][u][h] = *reinterpret_cast<const u32x4*>(piece + row * 128 +
+                                                     ((slot ^ lin_swz<128>(row)) << 4));
+    }
+  }
+}
+
+template <typename WT>
+using PpAcc = f32x4[PpTypes<WT>::kW][PpTypes<WT>::kX];
+
+template <typename WT>
+__device__ __forceinline__ void pp_mma(const PpFrags<WT>& f, int j, PpAcc<WT>& acc) {
+  using P = PpTypes<WT>;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(WT) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < P::kW; ++t)
+#pragma unroll
+          for (int u = 0; u < P::kX; ++u)
+            acc[t][u] = mfma16x16x4f32(__uint_as_float(f.w[t][h][i]),
+                                       __uint_as_float(f.x[j][u][h][i]), acc[t][u]);
+    } else {
+#pragma unroll
+      for (int t = 0; t < P::kW; ++t) {
+        bf16x8 w;
+        if constexpr (sizeof(WT) == 2)
+          w = __builtin_bit_cast(bf16x8, f.w[t][h]);
+        else
+          w = as_frag(e4m3x8_to_frag_bits(f.w[t][0][2 * h], f.w[t][0][2 * h + 1]));
+#pragma unroll
+        for (int u = 0; u < P::kX; ++u)
+          acc[t][u] = mfma16x16x32(w, __builtin_bit_cast(bf16x8, f.x[j][u][h]), acc[t][u]);
+      }
+    }
+  }
+}
+
+template <typename WT, bool kGated>
+struct PpTile {
+  using P = PpTypes<WT>;
+  using AT = typename P::AT;
+  using LW = PpLoader<WT, P::kWRow>;
+  using LX = PpLoader<AT, 128>;
+  const LW& lw;
+  const LX& lx;
+  int wrow, xrow;  // this wave's first row in a piece
+  int k_begin, k_end;
+
+  // One stage from the pieces w0, w1, x0, x1, loading the next stage (K from
+  // kn) into n*.  kLast: there is none.
+  template <bool kLast>
+  __device__ __forceinline__ void stage(const uint8_t* w0, const uint8_t* w1, const uint8_t* x0,
+                                        const uint8_t* x1, uint8_t* nw0, uint8_t* nw1, uint8_t* nx0,
+                                        uint8_t* nx1, int kn, PpFrags<WT>& f,
+                                        PpAcc<WT> (&acc)[2][2]) const {
+    constexpr int W = LW::kLoads, X = LX::kLoads;
+    // quadrant (0, 0); x1 has landed after it
+    pp_read_x<WT>(f, 0, x0, xrow);
+    pp_read_w<WT>(f, w0, wrow);
+    if (!kLast) {
+      lw.issue(0, nw0, kn, k_end);
+      lx.issue(0, nx0, kn, k_end);
+    }
+    pp_wait_loads<kLast ? W : 2 * W + X>();
+    matrix(f, 0, acc[0][0]);
+    // (0, 1); w1
+    pp_read_x<WT>(f, 1, x1, xrow);
+    if (!kLast) lx.issue(1, nx1, kn, k_end);
+    pp_wait_loads<kLast ? 0 : W + 2 * X>();
+    matrix(f, 1, acc[0][1]);
+    // (1, 1)
+    pp_read_w<WT>(f, w1, wrow);
+    if (!kLast) lw.issue(1, nw1, kn, k_end);
+    matrix(f, 1, acc[1][1]);
+    // (1, 0); the next stage's w0 and x0
+    if (!kLast) pp_wait_loads<W + X>();
+    matrix(f, 0, acc[1][0]);
+  }
+
+  __device__ __forceinline__ void matrix(const PpFrags<WT>& f, int j, PpAcc<WT>& acc) const {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    pp_barrier();
+    __builtin_amdgcn_s_setprio(1);
+    pp_mma<WT>(f, j, acc);
+    __builtin_amdgcn_s_setprio(0);
+    pp_barrier();
+  }
+};
+
+// Workgroup p's tile: contiguous runs of the logical order per XCD
+// (workgroup p runs on XCD p mod 8), in super-rows of kCols channel tiles
+// with the token tiles inside, so that the tiles an XCD runs together share
+// weight rows and token rows in its L2.
+__device__ __forceinline__ bool lin_raster(int p, int gx, int gy, int cols, int* tx, int* ty) {
+  const int total = gx * gy, per = (total + 7) / 8;
+  const int l = p % 8 * per + p / 8;
+  if (p / 8 >= per || l >= total) return false;
+  const int band = cols * gx, sr = l / band, rem = l - sr * band;
+  const int c = min(cols, gy - sr * cols);
+  *tx = rem / c;
+  *ty = sr * cols + rem % c;
+  return true;
+}
+
+// A wave's sums of 32 tokens into rows of `sums`.
+template <typename WT>
+__device__ __forceinline__ void pp_put(f32x4 (*sums)[64], const PpAcc<WT>& a0, const PpAcc<WT>& a1,
+                                       int wm, int r16, int g) {
+#pragma unroll
+  for (int u = 0; u < PpTypes<WT>::kX; ++u)
+#pragma unroll
+    for (int t = 0; t < PpTypes<WT>::kW; ++t) {
+      sums[16 * u + r16][(16 * wm + 4 * t + g) ^ r16] = a0[t][u];
+      sums[16 * u + r16][(32 + 16 * wm + 4 * t + g) ^ r16] = a1[t][u];
+    }
+}
+
+// Finishes the 32 tokens from m0 on held in `sums`.
+template <typename AT, bool kGated, int kCh>
+__device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sums)[64], int64_t m0,
+                                          int n0) {
+  constexpr int kQuads = kCh / 4;
+#pragma unroll 1
+  for (int o = threadIdx.x; o < 32 * kQuads; o += kPpThreads) {
+    const int row = o / kQuads, q = o % kQuads;
+    if (m0 + row >= a.M || n0 + 4 * q >= a.N) continue;
+    const f32x4 zg = sums[row][q ^ (row & 15)];
+    const f32x4 zu = kGated ? sums[row][(kQuads + q) ^ (row & 15)] : zg;
+    lin_store4<AT, kGated>(a, zg, zu, m0 + row, n0 + 4 * q);
+  }
+}
+
+template <typename WT, bool kGated>
+__global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, int gx, int gy) {
+  using P = PpTypes<WT>;
+  using AT = typename P::AT;
+  using T = PpTile<WT, kGated>;
+  constexpr int kWP = kPpPiece * P::kWRow, kXP = kPpPiece * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t w00[kWP], w01[kWP], x00[kXP], x01[kXP];
+  __shared__ __attribute__((aligned(1024))) uint8_t w10[kWP], w11[kWP], x10[kXP], x11[kXP];
+  __shared__ __attribute__((aligned(1024))) f32x4 sums[32][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int kCh = kGated ? kPpPiece : 2 * kPpPiece;  // channels of a tile
+  int tx, ty;
+  if (!lin_raster(blockIdx.x, gx, gy, 4, &tx, &ty)) return;  // uniform
+  const int n0 = ty * kCh;
+  const int64_t m0 = static_cast<int64_t>(tx) * 256;
+  const int k_begin = blockIdx.z * a.ksplit;
+  const int k_end = min(a.K, k_begin + a.ksplit);
+
+  typename T::LW lw;
+  const uint8_t* wb = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * a.ldw * sizeof(WT);
+  const size_t second = static_cast<size_t>(kGated ? a.N : kPpPiece) * a.ldw * sizeof(WT);
+  lw.init(wb, wb + second, a.N - n0, a.N - n0 - (kGated ? 0 : kPpPiece), a.ldw, a.K);
+  typename T::LX lx;
+  const uint8_t* xb = static_cast<const uint8_t*>(a.x) + m0 * a.ldx * sizeof(AT);
+  lx.init(xb, xb + kPpPiece * a.ldx * sizeof(AT), a.M - m0, a.M - m0 - kPpPiece, a.ldx, a.K);
+
+  const int wm = wave & 1, wn = wave >> 1;  // weight rows, tokens
+  const T tile{lw, lx, 64 * wm, 32 * wn, k_begin, k_end};
+  PpAcc<WT> acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int t = 0; t < P::kW; ++t)
+#pragma unroll
+        for (int u = 0; u < P::kX; ++u) acc[i][j][t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+  PpFrags<WT> f;
+
+  lw.issue(0, w00, k_begin, k_end);
+  lx.issue(0, x00, k_begin, k_end);
+  lx.issue(1, x01, k_begin, k_end);
+  lw.issue(1, w01, k_begin, k_end);
+  pp_wait_loads<T::LW::kLoads + T::LX::kLoads>();
+  pp_barrier();
+  const bool late = wave >= 4;  // one barrier behind
+  if (late) pp_barrier();
+  // two stages at a time (an odd count's last one reads zeros), the last two
+  // outside the loop
+  int k = k_begin;
+  for (; k + 2 * P::kKC < k_end; k += 2 * P::kKC) {
+    tile.template stage<false>(w00, w01, x00, x01, w10, w11, x10, x11, k + P::kKC, f, acc);
+    tile.template stage<false>(w10, w11, x10, x11, w00, w01, x00, x01, k + 2 * P::kKC, f, acc);
+  }
+  tile.template stage<false>(w00, w01, x00, x01, w10, w11, x10, x11, k + P::kKC, f, acc);
+  tile.template stage<true>(w10, w11, x10, x11, w00, w01, x00, x01, 0, f, acc);
+  if (!late) pp_barrier();
+
+  // The sums leave through LDS, 32 tokens (the two waves of one wn) at a
+  // time, so that every wave finishes and stores whole rows and the epilogue
+  // is one short loop.  A row is the tile's 256 sums of a token, its 16-byte
+  // units swizzled by the token.
+  const int r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    for (int r = 0; r < 4; ++r) {
+      __syncthreads();
+      if (wn == r) pp_put<WT>(sums, acc[0][j], acc[1][j], wm, r16, g);
+      __syncthreads();
+      pp_finish<AT, kGated, kCh>(a, sums, m0 + 128 * j + 32 * r, n0);
+    }
 }
 
 // ------------------------------------------------------------ few tokens
@@ -443,6 +806,18 @@ static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
   return a.gated ? launch_stream<WT, true>(a, s) : launch_stream<WT, false>(a, s);
 }
 
+template <typename WT>
+static hipError_t launch_pp(const LinearArgs& a, hipStream_t s) {
+  const int ch = a.gated ? kPpPiece : 2 * kPpPiece;
+  const int gx = static_cast<int>((a.M + 255) / 256), gy = (a.N + ch - 1) / ch;
+  const dim3 grid((gx * gy + 7) / 8 * 8, 1, a.splits);
+  if (a.gated)
+    linear_pp_kernel<WT, true><<<grid, kPpThreads, 0, s>>>(a, gx, gy);
+  else
+    linear_pp_kernel<WT, false><<<grid, kPpThreads, 0, s>>>(a, gx, gy);
+  return hipGetLastError();
+}
+
 template <typename WT, class G>
 static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
   const int tn = a.gated ? G::TN / 2 : G::TN;
@@ -464,18 +839,20 @@ size_t linear_part_bytes(const LinearArgs& a) {
   return a.splits > 1 ? static_cast<size_t>(a.splits) * a.M * a.R * 4 : 0;
 }
 
+template <typename WT>
+static hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
+  if (a.M <= kLinStreamTokens) return launch_stream<WT>(a, s);
+  constexpr int esz = 16 / (int)sizeof(WT), xsz = 16 / (int)sizeof(typename StreamGeom<WT>::AT);
+  const bool aligned = a.ldw % esz == 0 && a.ldx % xsz == 0 && a.K % esz == 0;
+  if (aligned && a.M >= 128) return launch_pp<WT>(a, s);
+  return launch_staged<WT, LinGeom<WT, 2, 2, 2, 2>>(a, s);
+}
+
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
-  if (a.M <= kLinStreamTokens) {
-    switch (a.w_dtype) {
-      case kDtypeF32: return launch_stream<float>(a, s);
-      case kDtypeBF16: return launch_stream<bf16_t>(a, s);
-      case kDtypeE4M3FN: return launch_stream<fp8_t>(a, s);
-    }
-  }
   switch (a.w_dtype) {
-    case kDtypeF32: return launch_staged<float, LinGeom<float, 2, 2, 2, 2>>(a, s);
-    case kDtypeBF16: return launch_staged<bf16_t, LinGeom<bf16_t, 2, 2, 2, 2>>(a, s);
-    case kDtypeE4M3FN: return launch_staged<fp8_t, LinGeom<fp8_t, 2, 2, 2, 2>>(a, s);
+    case kDtypeF32: return launch_type<float>(a, s);
+    case kDtypeBF16: return launch_type<bf16_t>(a, s);
+    case kDtypeE4M3FN: return launch_type<fp8_t>(a, s);
   }
   return hipErrorInvalidValue;
 }
