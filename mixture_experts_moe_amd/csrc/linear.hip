@@ -335,20 +335,25 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
 //
 // 256 weight rows x 256 tokens per workgroup, eight waves of 128 x 64 (two
 // per SIMD), each wave's tile in four quadrants of 64 x 32.  A K stage of
-// 128-byte rows is four pieces of 128 rows (the rows of quadrant row 0 and 1,
-// the tokens of quadrant column 0 and 1; gated: gate rows and up rows), each
-// in an LDS array of its own, two buffers.  A stage runs in four phases, one
-// per quadrant:
-//   load part:    the phase's new fragments LDS -> registers; the direct-to-
-//                 LDS loads of one or two pieces of the next stage; a wait for
-//                 the piece that the next phase reads
+// 128-byte rows is four pieces of 128 rows (weight rows w0, w1 of the quadrant
+// rows; gated: gate rows and up rows; tokens x0, x1 of the quadrant columns),
+// each in an LDS array of its own, two buffers.  A stage runs in four phases,
+// one per quadrant:
+//   load part:    fragments LDS -> registers (eight or four 16-byte reads); the
+//                 direct-to-LDS loads of one piece; a wait for the piece that
+//                 the next phase reads
 //   matrix part:  the quadrant's MFMAs
 // with a workgroup barrier after each part.  The waves of one half of the
 // workgroup run one barrier behind the others: on every SIMD one wave's
 // MFMAs run while the other loads, with the matrix wave's priority raised.
-// A piece is loaded three to four phases (about a microsecond) before it is
-// read.  Rows past M or N and K past the end read from past the end of their
-// buffer resource: zeros, without a memory access.
+// The quadrants go (0,f) (0,o) (1,o) (1,f) with f the stage's first token
+// column, 0 in even stages and 1 in odd ones, so that the last phase can read
+// the next stage's first tokens into the registers that have just become
+// free, and every phase reads at most eight fragments.  A piece of the stage
+// after the next is loaded as soon as both halves have read the piece it
+// replaces, six phases (over a microsecond) before it is read.  Rows past M
+// or N and K past the end read from past the end of their buffer resource:
+// zeros, without a memory access.
 
 constexpr int kPpThreads = 512;
 constexpr int kPpPiece = 128;  // rows of a piece
@@ -505,35 +510,34 @@ struct PpTile {
   int wrow, xrow;  // this wave's first row in a piece
   int k_begin, k_end;
 
-  // One stage from the pieces w0, w1, x0, x1, loading the next stage (K from
-  // kn) into n*.  kLast: there is none.
-  template <bool kLast>
-  __device__ __forceinline__ void stage(const uint8_t* w0, const uint8_t* w1, const uint8_t* x0,
-                                        const uint8_t* x1, uint8_t* nw0, uint8_t* nw1, uint8_t* nx0,
-                                        uint8_t* nx1, int kn, PpFrags<WT>& f,
+  // One stage from the pieces w0, w1, x0, x1; its first tokens are already in
+  // registers, those of the next stage (piece nx of the other buffer) are
+  // read.  kTail: 0 loads the stage after the next (K from kn) into the
+  // pieces just read; 1, 2: the last stage but one, the last.
+  template <int kFirst, int kTail>
+  __device__ __forceinline__ void stage(uint8_t* w0, uint8_t* w1, uint8_t* x0, uint8_t* x1,
+                                        const uint8_t* nx, int kn, PpFrags<WT>& f,
                                         PpAcc<WT> (&acc)[2][2]) const {
-    constexpr int W = LW::kLoads, X = LX::kLoads;
-    // quadrant (0, 0); x1 has landed after it
-    pp_read_x<WT>(f, 0, x0, xrow);
+    constexpr int W = LW::kLoads, X = LX::kLoads, O = 1 - kFirst;
+    uint8_t* const xf = kFirst ? x1 : x0;
+    uint8_t* const xo = kFirst ? x0 : x1;
+    // the loads issued after the piece that must have landed may be in flight
     pp_read_w<WT>(f, w0, wrow);
-    if (!kLast) {
-      lw.issue(0, nw0, kn, k_end);
-      lx.issue(0, nx0, kn, k_end);
-    }
-    pp_wait_loads<kLast ? W : 2 * W + X>();
-    matrix(f, 0, acc[0][0]);
-    // (0, 1); w1
-    pp_read_x<WT>(f, 1, x1, xrow);
-    if (!kLast) lx.issue(1, nx1, kn, k_end);
-    pp_wait_loads<kLast ? 0 : W + 2 * X>();
-    matrix(f, 1, acc[0][1]);
-    // (1, 1)
+    if (kTail == 0) lx.issue(kFirst, xf, kn, k_end);
+    pp_wait_loads<kTail == 0 ? 3 * W + 3 * X : kTail == 1 ? 3 * W + 2 * X : W>();  // xo
+    matrix(f, kFirst, acc[0][kFirst]);
+    pp_read_x<WT>(f, O, xo, xrow);
+    if (kTail == 0) lw.issue(0, w0, kn, k_end);
+    pp_wait_loads<kTail == 0 ? 3 * W + 3 * X : kTail == 1 ? 2 * W + 2 * X : 0>();  // w1
+    matrix(f, O, acc[0][O]);
     pp_read_w<WT>(f, w1, wrow);
-    if (!kLast) lw.issue(1, nw1, kn, k_end);
-    matrix(f, 1, acc[1][1]);
-    // (1, 0); the next stage's w0 and x0
-    if (!kLast) pp_wait_loads<W + X>();
-    matrix(f, 0, acc[1][0]);
+    if (kTail == 0) lx.issue(O, xo, kn, k_end);
+    if (kTail < 2) pp_wait_loads<kTail == 0 ? 3 * W + 3 * X : 2 * W + X>();  // nx
+    matrix(f, O, acc[1][O]);
+    if (kTail < 2) pp_read_x<WT>(f, O, nx, xrow);
+    if (kTail == 0) lw.issue(1, w1, kn, k_end);
+    if (kTail < 2) pp_wait_loads<kTail == 0 ? 3 * W + 3 * X : W + X>();  // the next w0
+    matrix(f, kFirst, acc[1][kFirst]);
   }
 
   __device__ __forceinline__ void matrix(const PpFrags<WT>& f, int j, PpAcc<WT>& acc) const {
@@ -574,19 +578,25 @@ __device__ __forceinline__ void pp_put(f32x4 (*sums)[64], const PpAcc<WT>& a0, c
     }
 }
 
-// Finishes the 32 tokens from m0 on held in `sums`.
+// Finishes the 32 tokens from m0 on held in `sums`: a thread takes the same
+// four channels of every 8th (gated: 16th) token.
 template <typename AT, bool kGated, int kCh>
 __device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sums)[64], int64_t m0,
                                           int n0) {
-  constexpr int kQuads = kCh / 4;
-#pragma unroll 1
-  for (int o = threadIdx.x; o < 32 * kQuads; o += kPpThreads) {
-    const int row = o / kQuads, q = o % kQuads;
-    if (m0 + row >= a.M || n0 + 4 * q >= a.N) continue;
-    const f32x4 zg = sums[row][q ^ (row & 15)];
-    const f32x4 zu = kGated ? sums[row][(kQuads + q) ^ (row & 15)] : zg;
-    lin_store4<AT, kGated>(a, zg, zu, m0 + row, n0 + 4 * q);
+  constexpr int kQuads = kCh / 4, kStep = kPpThreads / kQuads, kRows = 32 / kStep;
+  const int q = threadIdx.x % kQuads, row0 = threadIdx.x / kQuads;
+  if (n0 + 4 * q >= a.N) return;
+  f32x4 zg[kRows], zu[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = row0 + i * kStep;
+    zg[i] = sums[row][q ^ (row & 15)];
+    zu[i] = kGated ? sums[row][(kQuads + q) ^ (row & 15)] : zg[i];
   }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (m0 + row0 + i * kStep < a.M)
+      lin_store4<AT, kGated>(a, zg[i], zu[i], m0 + row0 + i * kStep, n0 + 4 * q);
 }
 
 template <typename WT, bool kGated>
@@ -629,23 +639,31 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
         for (int u = 0; u < P::kX; ++u) acc[i][j][t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
   PpFrags<WT> f;
 
-  lw.issue(0, w00, k_begin, k_end);
+  constexpr int KC = P::kKC;
   lx.issue(0, x00, k_begin, k_end);
+  lw.issue(0, w00, k_begin, k_end);
   lx.issue(1, x01, k_begin, k_end);
   lw.issue(1, w01, k_begin, k_end);
-  pp_wait_loads<T::LW::kLoads + T::LX::kLoads>();
+  lx.issue(1, x11, k_begin + KC, k_end);
+  lw.issue(0, w10, k_begin + KC, k_end);
+  lx.issue(0, x10, k_begin + KC, k_end);
+  lw.issue(1, w11, k_begin + KC, k_end);
+  pp_wait_loads<3 * (T::LW::kLoads + T::LX::kLoads)>();  // stage 0's x0 and w0
   pp_barrier();
+  pp_read_x<WT>(f, 0, x00, tile.xrow);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  pp_barrier();  // x00 may be overwritten
   const bool late = wave >= 4;  // one barrier behind
   if (late) pp_barrier();
   // two stages at a time (an odd count's last one reads zeros), the last two
   // outside the loop
   int k = k_begin;
-  for (; k + 2 * P::kKC < k_end; k += 2 * P::kKC) {
-    tile.template stage<false>(w00, w01, x00, x01, w10, w11, x10, x11, k + P::kKC, f, acc);
-    tile.template stage<false>(w10, w11, x10, x11, w00, w01, x00, x01, k + 2 * P::kKC, f, acc);
+  for (; k + 2 * KC < k_end; k += 2 * KC) {
+    tile.template stage<0, 0>(w00, w01, x00, x01, x11, k + 2 * KC, f, acc);
+    tile.template stage<1, 0>(w10, w11, x10, x11, x00, k + 3 * KC, f, acc);
   }
-  tile.template stage<false>(w00, w01, x00, x01, w10, w11, x10, x11, k + P::kKC, f, acc);
-  tile.template stage<true>(w10, w11, x10, x11, w00, w01, x00, x01, 0, f, acc);
+  tile.template stage<0, 1>(w00, w01, x00, x01, x11, 0, f, acc);
+  tile.template stage<1, 2>(w10, w11, x10, x11, nullptr, 0, f, acc);
   if (!late) pp_barrier();
 
   // The sums leave through LDS, 32 tokens (the two waves of one wn) at a
