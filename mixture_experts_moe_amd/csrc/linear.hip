@@ -19,29 +19,25 @@ namespace moe {
 // z / (1 + e^-u): no cancellation for large negative z, exp overflow gives a
 // quotient of zero.
 
+// With bf16 results the sigmoids use the hardware's exp2 and reciprocal
+// (within 2^-18 of the exact quotient for any |z| below 64: a thousandth of
+// the result's half step).
+template <bool kFast>
+__device__ __forceinline__ float lin_sigmoid_times(float z, float u) {  // z / (1 + e^-u)
+  if constexpr (kFast) return z * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+  return z / (1.0f + expf(-u));
+}
+
+template <bool kFast>
 __device__ __forceinline__ float lin_act(int fn, float z) {
   switch (fn) {
     case kFnRelu: return z < 0.f ? 0.f : z;  // NaN stays
-    case kFnSilu: return silu(z);
+    case kFnSilu: return lin_sigmoid_times<kFast>(z, z);
     case kFnGelu: return 0.5f * z * erfcf(z * -0.70710678118654752f);
     case kFnGeluTanh:  // tanh(u) = 2 / (1 + e^-2u) - 1, u = sqrt(2/pi) (z + 0.044715 z^3)
-      return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+      return lin_sigmoid_times<kFast>(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
   }
   return z;
-}
-
-// One output element from its channel sums (zu: the up half's, when gated).
-__device__ __forceinline__ float lin_value(const LinearArgs& a, float zg, float zu, int n) {
-  if (a.scale) {
-    zg *= a.scale_channel ? a.scale[n] : a.scale[0];
-    if (a.gated) zu *= a.scale_channel ? a.scale[a.N + n] : a.scale[0];
-  }
-  if (a.bias) {
-    zg += a.bias[n];
-    if (a.gated) zu += a.bias[a.N + n];
-  }
-  const float y = lin_act(a.fn, zg);
-  return a.gated ? y * zu : y;
 }
 
 template <typename AT>
@@ -60,60 +56,122 @@ __device__ __forceinline__ void lin_store(AT* p, float v) {
     *p = f32_to_bf16(v);
 }
 
-// Finish and store out[m, n] (residual read and result written by one
-// thread, so out may be the residual itself).
+// Finish and store out[m, n] from its channel sums (zu: the up half's, when
+// gated).  The residual is read and the result written by one thread, so out
+// may be the residual itself.
 template <typename AT>
 __device__ __forceinline__ void lin_finish(const LinearArgs& a, float zg, float zu, int64_t m,
                                            int n) {
-  float v = lin_value(a, zg, zu, n);
+  if (a.scale) {
+    zg *= a.scale_channel ? a.scale[n] : a.scale[0];
+    if (a.gated) zu *= a.scale_channel ? a.scale[a.N + n] : a.scale[0];
+  }
+  if (a.bias) {
+    zg += a.bias[n];
+    if (a.gated) zu += a.bias[a.N + n];
+  }
+  float v = lin_act<sizeof(AT) == 2>(a.fn, zg);
+  if (a.gated) v *= zu;
   if (a.res) v += lin_load(static_cast<const AT*>(a.res) + m * a.ldr + n);
   lin_store(static_cast<AT*>(a.out) + m * a.ldo + n, v);
 }
 
-// Four consecutive channels n .. n+3 of token m (those below N): finished
-// outputs, or this K range's sums where K is split.
+// Four consecutive channels n .. n+3 (those below N) for several tokens: the
+// scales and biases are read once.
 template <typename AT, bool kGated>
-__device__ __forceinline__ void lin_store4(const LinearArgs& a, f32x4 zg, f32x4 zu, int64_t m,
-                                           int n) {
-  if (a.part) {
+struct LinQuad {
+  f32x4 sg, su, bg, bu;
+  int n, valid;  // channels that exist
+
+  __device__ __forceinline__ void init(const LinearArgs& a, int n_) {
+    n = n_;
+    valid = min(a.N - n, 4);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int c = min(n + v, a.N - 1);
+      sg[v] = !a.scale ? 1.f : a.scale[a.scale_channel ? c : 0];
+      bg[v] = a.bias ? a.bias[c] : 0.f;
+      if (kGated) {
+        su[v] = !a.scale ? 1.f : a.scale[a.scale_channel ? a.N + c : 0];
+        bu[v] = a.bias ? a.bias[a.N + c] : 0.f;
+      }
+    }
+  }
+
+  // kRows tokens' sums zg (and zu) -> values, with the function chosen once
+  template <int kRows>
+  __device__ __forceinline__ void values(const LinearArgs& a, f32x4 (&zg)[kRows],
+                                         f32x4 (&zu)[kRows]) const {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      zg[i] = zg[i] * sg + bg;
+      if (kGated) zu[i] = zu[i] * su + bu;
+    }
+    auto apply = [&](int fn) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) zg[i][v] = lin_act<sizeof(AT) == 2>(fn, zg[i][v]);
+    };
+    switch (a.fn) {
+      case kFnRelu: apply(kFnRelu); break;
+      case kFnSilu: apply(kFnSilu); break;
+      case kFnGeluTanh: apply(kFnGeluTanh); break;
+      case kFnGelu:  // a long function: one copy
+#pragma unroll 1
+        for (int i = 0; i < 4 * kRows; ++i) {
+          float z = zg[0][0];
+#pragma unroll
+          for (int j = 1; j < 4 * kRows; ++j) z = i == j ? zg[j / 4][j % 4] : z;
+          z = lin_act<sizeof(AT) == 2>(kFnGelu, z);
+#pragma unroll
+          for (int j = 0; j < 4 * kRows; ++j) zg[j / 4][j % 4] = i == j ? z : zg[j / 4][j % 4];
+        }
+        break;
+    }
+    if (kGated) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) zg[i] *= zu[i];
+    }
+  }
+
+  // + residual, rounded, stored
+  __device__ __forceinline__ void store(const LinearArgs& a, f32x4 z, int64_t m) const {
+    AT* o = static_cast<AT*>(a.out) + m * a.ldo + n;
+    const AT* r = static_cast<const AT*>(a.res) + m * a.ldr + n;
+    if (a.vec4 && valid == 4) {
+      if constexpr (sizeof(AT) == 4) {
+        if (a.res) z += *reinterpret_cast<const f32x4*>(r);
+        *reinterpret_cast<f32x4*>(o) = z;
+      } else {
+        if (a.res) {
+          const uint2 q = *reinterpret_cast<const uint2*>(r);
+          z += f32x4{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
+                     __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)};
+        }
+        *reinterpret_cast<uint2*>(o) =
+            uint2{f32_to_bf16(z[0]) | (static_cast<uint32_t>(f32_to_bf16(z[1])) << 16),
+                  f32_to_bf16(z[2]) | (static_cast<uint32_t>(f32_to_bf16(z[3])) << 16)};
+      }
+      return;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (v < valid) lin_store(o + v, a.res ? z[v] + lin_load(r + v) : z[v]);
+  }
+
+  // the sums of this K range instead, where K is split
+  __device__ __forceinline__ void store_part(const LinearArgs& a, f32x4 zg, f32x4 zu,
+                                             int64_t m) const {
     float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      if (n + v < a.N) {
+      if (v < valid) {
         p[n + v] = zg[v];
         if (kGated) p[a.N + n + v] = zu[v];
       }
-    return;
   }
-  if (a.vec4 && n + 4 <= a.N) {  // rows and residual rows in whole vectors
-    AT* o = static_cast<AT*>(a.out) + m * a.ldo + n;
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lin_value(a, zg[i], kGated ? zu[i] : 0.f, n + i);
-    if constexpr (sizeof(AT) == 4) {
-      if (a.res) {
-        const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.res) +
-                                                          m * a.ldr + n);
-        v[0] += r.x, v[1] += r.y, v[2] += r.z, v[3] += r.w;
-      }
-      *reinterpret_cast<float4*>(o) = float4{v[0], v[1], v[2], v[3]};
-    } else {
-      if (a.res) {
-        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const bf16_t*>(a.res) +
-                                                        m * a.ldr + n);
-        v[0] += __uint_as_float(r.x << 16), v[1] += __uint_as_float(r.x & 0xffff0000u);
-        v[2] += __uint_as_float(r.y << 16), v[3] += __uint_as_float(r.y & 0xffff0000u);
-      }
-      *reinterpret_cast<uint2*>(o) =
-          uint2{f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16),
-                f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16)};
-    }
-    return;
-  }
-#pragma unroll
-  for (int v = 0; v < 4; ++v)
-    if (n + v < a.N) lin_finish<AT>(a, zg[v], kGated ? zu[v] : 0.f, m, n + v);
-}
+};
 
 // ------------------------------------------------------------ tiled product
 //
@@ -262,13 +320,28 @@ __device__ __forceinline__ void lin_epilogue(const LinearArgs& a, LinAcc<G>& acc
   const int r16 = lane & 15, g = lane >> 4;
   constexpr int H = kGated ? G::TA / 2 : G::TA;
 #pragma unroll
-  for (int u = 0; u < G::TB; ++u) {
-    const int64_t m = m0 + 16 * (G::TB * wm + u) + r16;
-    if (m >= a.M) continue;
+  for (int t = 0; t < H; ++t) {
+    const int n = n0 + lin_tile_row<G, kGated>(wn, t) + 4 * g;
+    LinQuad<AT, kGated> quad;
+    if (n < a.N) {
+      quad.init(a, n);
+      f32x4 zg[G::TB], zu[G::TB];
 #pragma unroll
-    for (int t = 0; t < H; ++t) {
-      const int n = n0 + lin_tile_row<G, kGated>(wn, t) + 4 * g;
-      lin_store4<AT, kGated>(a, acc[t][u], acc[(t + H) % G::TA][u], m, n);
+      for (int u = 0; u < G::TB; ++u) {
+        zg[u] = acc[t][u];
+        zu[u] = acc[(t + H) % G::TA][u];
+      }
+      if (!a.part) quad.template values<G::TB>(a, zg, zu);
+#pragma unroll
+      for (int u = 0; u < G::TB; ++u) {
+        const int64_t m = m0 + 16 * (G::TB * wm + u) + r16;
+        if (m < a.M) {
+          if (a.part)
+            quad.store_part(a, zg[u], zu[u], m);
+          else
+            quad.store(a, zg[u], m);
+        }
+      }
     }
   }
 }
@@ -581,11 +654,10 @@ __device__ __forceinline__ void pp_put(f32x4 (*sums)[64], const PpAcc<WT>& a0, c
 // Finishes the 32 tokens from m0 on held in `sums`: a thread takes the same
 // four channels of every 8th (gated: 16th) token.
 template <typename AT, bool kGated, int kCh>
-__device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sums)[64], int64_t m0,
-                                          int n0) {
+__device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sums)[64],
+                                          const LinQuad<AT, kGated>& quad, int64_t m0) {
   constexpr int kQuads = kCh / 4, kStep = kPpThreads / kQuads, kRows = 32 / kStep;
   const int q = threadIdx.x % kQuads, row0 = threadIdx.x / kQuads;
-  if (n0 + 4 * q >= a.N) return;
   f32x4 zg[kRows], zu[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -593,10 +665,16 @@ __device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sum
     zg[i] = sums[row][q ^ (row & 15)];
     zu[i] = kGated ? sums[row][(kQuads + q) ^ (row & 15)] : zg[i];
   }
+  if (a.part) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (m0 + row0 + i * kStep < a.M) quad.store_part(a, zg[i], zu[i], m0 + row0 + i * kStep);
+    return;
+  }
+  quad.template values<kRows>(a, zg, zu);
 #pragma unroll
   for (int i = 0; i < kRows; ++i)
-    if (m0 + row0 + i * kStep < a.M)
-      lin_store4<AT, kGated>(a, zg[i], zu[i], m0 + row0 + i * kStep, n0 + 4 * q);
+    if (m0 + row0 + i * kStep < a.M) quad.store(a, zg[i], m0 + row0 + i * kStep);
 }
 
 template <typename WT, bool kGated>
@@ -671,14 +749,21 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
   // is one short loop.  A row is the tile's 256 sums of a token, its 16-byte
   // units swizzled by the token.
   const int r16 = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    for (int r = 0; r < 4; ++r) {
-      __syncthreads();
-      if (wn == r) pp_put<WT>(sums, acc[0][j], acc[1][j], wm, r16, g);
-      __syncthreads();
-      pp_finish<AT, kGated, kCh>(a, sums, m0 + 128 * j + 32 * r, n0);
+  LinQuad<AT, kGated> quad;
+  const int nq = n0 + 4 * static_cast<int>(threadIdx.x % (kCh / 4));
+  if (nq < a.N) quad.init(a, nq);
+#pragma unroll 1
+  for (int r = 0; r < 8; ++r) {
+    __syncthreads();
+    if (wn == (r & 3)) {
+      if (r < 4)
+        pp_put<WT>(sums, acc[0][0], acc[1][0], wm, r16, g);
+      else
+        pp_put<WT>(sums, acc[0][1], acc[1][1], wm, r16, g);
     }
+    __syncthreads();
+    if (nq < a.N) pp_finish<AT, kGated, kCh>(a, sums, quad, m0 + 32 * r);
+  }
 }
 
 // ------------------------------------------------------------ few tokens
