@@ -240,11 +240,13 @@ struct LinearArgs {
   int act_dtype, w_dtype, fn;
   bool gated, scale_channel;
   bool vec4;           // out (and residual) rows hold aligned vectors of four
+  int tile;            // the kernel that runs (linear_plan)
   int splits;          // K ranges, each ksplit long (the last may be shorter)
   int ksplit;
 };
 
-// Chooses the K split (the other fields set, pointers not yet needed).
+// Chooses the kernel and the K split (the other fields set, pointers not yet
+// needed).
 void linear_plan(LinearArgs* a);
 size_t linear_part_bytes(const LinearArgs& a);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);

@@ -149,9 +149,9 @@ struct LinQuad {
           z += f32x4{__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u),
                      __uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u)};
         }
-        *reinterpret_cast<uint2*>(o) =
-            uint2{f32_to_bf16(z[0]) | (static_cast<uint32_t>(f32_to_bf16(z[1])) << 16),
-                  f32_to_bf16(z[2]) | (static_cast<uint32_t>(f32_to_bf16(z[3])) << 16)};
+        // the hardware's conversion: to nearest even, NaN kept
+        typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<bf16x4v*>(o) = __builtin_convertvector(z, bf16x4v);
       }
       return;
     }
@@ -163,12 +163,17 @@ struct LinQuad {
   // the sums of this K range instead, where K is split
   __device__ __forceinline__ void store_part(const LinearArgs& a, f32x4 zg, f32x4 zu,
                                              int64_t m) const {
-    float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R;
+    float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R + n;
+    if (a.N % 4 == 0) {
+      *reinterpret_cast<f32x4*>(p) = zg;
+      if (kGated) *reinterpret_cast<f32x4*>(p + a.N) = zu;
+      return;
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       if (v < valid) {
-        p[n + v] = zg[v];
-        if (kGated) p[a.N + n + v] = zu[v];
+        p[v] = zg[v];
+        if (kGated) p[a.N + v] = zu[v];
       }
   }
 };
@@ -374,8 +379,8 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
 
   const WT* w = static_cast<const WT*>(a.w);
   const AT* x = static_cast<const AT*>(a.x);
-  for (int k0 = k_begin; k0 < k_end; k0 += G::kKC) {
-    u32x4 wv[G::kWUnits], xv[G::kXUnits];
+  u32x4 wv[G::kWUnits], xv[G::kXUnits];
+  auto fetch = [&](int k0) {
 #pragma unroll
     for (int q = 0; q < G::kWUnits; ++q) {
       const int tr = q * G::kWRowsPerQ + tid / (G::kWRow / 16);
@@ -391,6 +396,9 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
       const int k = k0 + ((tid % 8) ^ lin_swz<G::kXRow>(tr)) * (16 / (int)sizeof(AT));
       xv[q] = m0 + tr < a.M ? lin_unit<AT>(x + (m0 + tr) * a.ldx, k, k_end) : u32x4{0, 0, 0, 0};
     }
+  };
+  fetch(k_begin);
+  for (int k0 = k_begin; k0 < k_end; k0 += G::kKC) {
     __syncthreads();  // the previous stage has been read
 #pragma unroll
     for (int q = 0; q < G::kWUnits; ++q)
@@ -399,6 +407,7 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
     for (int q = 0; q < G::kXUnits; ++q)
       *reinterpret_cast<u32x4*>(stage + G::kWBytes + 16 * (q * G::kThreads + tid)) = xv[q];
     __syncthreads();
+    if (k0 + G::kKC < k_end) fetch(k0 + G::kKC);  // in flight during the MFMAs
     lin_mma<WT, G>(stage, wrow, xrow, acc);
   }
   lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
@@ -429,6 +438,7 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
 // zeros, without a memory access.
 
 constexpr int kPpThreads = 512;
+constexpr int kPpCols = 4;  // channel tiles of a super-row of the raster
 constexpr int kPpPiece = 128;  // rows of a piece
 constexpr uint32_t kPpDead = 0x80000000u;  // an offset past every resource
 
@@ -690,7 +700,7 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kCh = kGated ? kPpPiece : 2 * kPpPiece;  // channels of a tile
   int tx, ty;
-  if (!lin_raster(blockIdx.x, gx, gy, 4, &tx, &ty)) return;  // uniform
+  if (!lin_raster(blockIdx.x, gx, gy, kPpCols, &tx, &ty)) return;  // uniform
   const int n0 = ty * kCh;
   const int64_t m0 = static_cast<int64_t>(tx) * 256;
   const int k_begin = blockIdx.z * a.ksplit;
@@ -764,6 +774,200 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
     __syncthreads();
     if (nq < a.N) pp_finish<AT, kGated, kCh>(a, sums, quad, m0 + 32 * r);
   }
+}
+
+// ------------------------------------------------------------ middle sizes
+//
+// LinGeom's tile with both operands by direct-to-LDS loads, through a ring of
+// S stages in LDS arrays of their own (reads of one stage then wait for no
+// load into another): S - 1 stages are in flight while one is multiplied, so
+// a workgroup alone on its compute unit covers the memory latency.
+
+// One operand of a tile: kRows rows, of which [0, kSplit) start at one base
+// and the rest at another (gated weights; else kSplit = kRows).
+template <typename T, int kRowBytes, int kThreads, int kRows, int kSplit>
+struct TileLoader {
+  static constexpr int kUnits = kRowBytes / 16;
+  static constexpr int kStep = kThreads / kUnits;             // rows per load
+  static constexpr int kLoads = kRows / kStep;                // per stage and thread
+  static_assert(kRows % kStep == 0 && kSplit % (64 / kUnits) == 0, "whole loads");
+  static_assert(kStep % 16 == 0, "one swizzle per thread");
+  __amdgpu_buffer_rsrc_t r[2];
+  uint32_t off[kLoads];
+  int ke;
+
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base,
+                                                                    int64_t rows, int64_t ld,
+                                                                    int K) {
+    const int64_t n = rows < kRows ? rows : kRows;
+    const int64_t bytes = n > 0 ? ((n - 1) * ld + K) * (int)sizeof(T) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                             static_cast<int>(bytes), 0x00020000);
+  }
+  __device__ __forceinline__ void init(const uint8_t* base0, const uint8_t* base1, int64_t rows,
+                                       int64_t ld, int K) {
+    const int row = threadIdx.x / kUnits;
+    ke = ((threadIdx.x % kUnits) ^ lin_swz<kRowBytes>(row)) * (16 / (int)sizeof(T));
+    r[0] = resource(base0, kSplit < kRows && rows > kSplit ? kSplit : rows, ld, K);
+    r[1] = resource(base1, rows > kSplit ? kSplit : rows, ld, K);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      off[q] = static_cast<uint32_t>((row + q * kStep) % kSplit * ld + ke) * (uint32_t)sizeof(T);
+  }
+  __device__ __forceinline__ void issue(uint8_t* lds, int k0, int k_end) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q)
+      lds_load16(q * kStep + wave * (64 / kUnits) >= kSplit ? r[1] : r[0],
+                 lds + (q * kThreads + 64 * wave) * 16,
+                 k0 + ke < k_end ? off[q] : kPpDead, k0 * (int)sizeof(T));
+  }
+};
+
+template <typename WT, class G, int S, bool kGated>
+__global__ __launch_bounds__(G::kThreads) void linear_tile_kernel(LinearArgs a, int gx, int gy) {
+  using AT = typename G::AT;
+  static_assert(S >= 2 && S <= 4, "ring depth");
+  constexpr int kCh = kGated ? G::TN / 2 : G::TN;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[G::kStage], s1[G::kStage],
+      s2[S > 2 ? G::kStage : 16], s3[S > 3 ? G::kStage : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tx, ty;
+  if (!lin_raster(blockIdx.x, gx, gy, kPpCols, &tx, &ty)) return;  // uniform
+  const int n0 = ty * kCh;
+  const int64_t m0 = static_cast<int64_t>(tx) * G::TM;
+  const int k_begin = blockIdx.z * a.ksplit;
+  const int k_end = min(a.K, k_begin + a.ksplit);
+  const int nst = (k_end - k_begin + G::kKC - 1) / G::kKC;
+
+  TileLoader<WT, G::kWRow, G::kThreads, G::TN, kCh> lw;
+  const uint8_t* wb = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * a.ldw * sizeof(WT);
+  lw.init(wb, wb + static_cast<size_t>(a.N) * a.ldw * sizeof(WT), a.N - n0, a.ldw, a.K);
+  TileLoader<AT, G::kXRow, G::kThreads, G::TM, G::TM> lx;
+  const uint8_t* xb = static_cast<const uint8_t*>(a.x) + m0 * a.ldx * sizeof(AT);
+  lx.init(xb, xb, a.M - m0, a.ldx, a.K);
+  constexpr int L = decltype(lw)::kLoads + decltype(lx)::kLoads;
+
+  const int wn = wave % G::WN, wm = wave / G::WN;
+  int wrow[G::TA], xrow[G::TB];
+#pragma unroll
+  for (int t = 0; t < G::TA; ++t) wrow[t] = lin_tile_row<G, kGated>(wn, t) + (lane & 15);
+#pragma unroll
+  for (int u = 0; u < G::TB; ++u) xrow[u] = 16 * (G::TB * wm + u) + (lane & 15);
+  LinAcc<G> acc;
+#pragma unroll
+  for (int t = 0; t < G::TA; ++t)
+#pragma unroll
+    for (int u = 0; u < G::TB; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto issue = [&](uint8_t* st, int i) {
+    lw.issue(st, k_begin + i * G::kKC, k_end);
+    lx.issue(st + G::kWBytes, k_begin + i * G::kKC, k_end);
+  };
+  // stage i, in `cur`; `prev` held stage i - 1, which everybody has read once
+  // past the barrier
+  auto step = [&](uint8_t* cur, uint8_t* prev, int i) {
+    if (i + S - 1 < nst) {
+      pp_wait_loads<L * (S - 2)>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      issue(prev, i + S - 1);
+    } else {
+      pp_wait_loads<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    lin_mma<WT, G>(cur, wrow, xrow, acc);
+  };
+  // the first stages go so that the last one is in the ring's last buffer and
+  // whole turns follow: stage i in buffer (i + first) % S
+  const int first = (S - nst % S) % S;
+  int i = 0;
+  if constexpr (S == 2) {
+    if (first == 0) {
+      issue(s0, 0);
+    } else {
+      issue(s1, 0);
+      step(s1, s0, 0);
+      i = 1;
+    }
+    for (; i < nst; i += 2) {
+      step(s0, s1, i);
+      step(s1, s0, i + 1);
+    }
+  } else if constexpr (S == 3) {
+    if (first == 0) {
+      issue(s0, 0), issue(s1, 1);
+    } else if (first == 1) {
+      issue(s1, 0), issue(s2, 1);
+      step(s1, s0, 0), step(s2, s1, 1);
+      i = 2;
+    } else {
+      issue(s2, 0);
+      if (nst > 1) issue(s0, 1);
+      step(s2, s1, 0);
+      i = 1;
+    }
+    for (; i < nst; i += 3) {
+      step(s0, s2, i);
+      step(s1, s0, i + 1);
+      step(s2, s1, i + 2);
+    }
+  } else {
+    if (first == 0) {
+      issue(s0, 0), issue(s1, 1), issue(s2, 2);
+    } else if (first == 1) {
+      issue(s1, 0), issue(s2, 1), issue(s3, 2);
+      step(s1, s0, 0), step(s2, s1, 1), step(s3, s2, 2);
+      i = 3;
+    } else if (first == 2) {
+      issue(s2, 0), issue(s3, 1);
+      if (nst > 2) issue(s0, 2);
+      step(s2, s1, 0), step(s3, s2, 1);
+      i = 2;
+    } else {
+      issue(s3, 0);
+      if (nst > 1) issue(s0, 1), issue(s1, 2);
+      step(s3, s2, 0);
+      i = 1;
+    }
+    for (; i < nst; i += 4) {
+      step(s0, s3, i);
+      step(s1, s0, i + 1);
+      step(s2, s1, i + 2);
+      step(s3, s2, i + 3);
+    }
+  }
+  lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
+}
+
+// The K ranges' sums of four channels of a token, added in order and finished.
+constexpr int kReduceThreads = 256;
+template <typename AT, bool kGated>
+__global__ __launch_bounds__(kReduceThreads) void linear_reduce_kernel(LinearArgs a) {
+  const int quads = (a.N + 3) / 4;
+  const int64_t o = static_cast<int64_t>(blockIdx.x) * kReduceThreads + threadIdx.x;
+  const int64_t m = o / quads;
+  if (m >= a.M) return;
+  LinQuad<AT, kGated> quad;
+  quad.init(a, static_cast<int>(o % quads) * 4);
+  f32x4 zg[1] = {f32x4{0.f, 0.f, 0.f, 0.f}}, zu[1] = {zg[0]};
+  for (int z = 0; z < a.splits; ++z) {
+    const float* p = a.part + (static_cast<size_t>(z) * a.M + m) * a.R + quad.n;
+    if (a.N % 4 == 0) {
+      zg[0] += *reinterpret_cast<const f32x4*>(p);
+      if (kGated) zu[0] += *reinterpret_cast<const f32x4*>(p + a.N);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (v < quad.valid) {
+          zg[0][v] += p[v];
+          if (kGated) zu[0][v] += p[a.N + v];
+        }
+    }
+  }
+  quad.template values<1>(a, zg, zu);
+  quad.store(a, zg[0], m);
 }
 
 // ------------------------------------------------------------ few tokens
@@ -921,6 +1125,29 @@ static hipError_t launch_pp(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename WT, class G, int S>
+static hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
+  const int ch = a.gated ? G::TN / 2 : G::TN;
+  const int gx = static_cast<int>((a.M + G::TM - 1) / G::TM), gy = (a.N + ch - 1) / ch;
+  const dim3 grid((gx * gy + 7) / 8 * 8, 1, a.splits);
+  if (a.gated)
+    linear_tile_kernel<WT, G, S, true><<<grid, G::kThreads, 0, s>>>(a, gx, gy);
+  else
+    linear_tile_kernel<WT, G, S, false><<<grid, G::kThreads, 0, s>>>(a, gx, gy);
+  return hipGetLastError();
+}
+
+template <typename AT>
+static hipError_t launch_reduce(const LinearArgs& a, hipStream_t s) {
+  const int64_t n = a.M * ((a.N + 3) / 4);
+  const unsigned grid = static_cast<unsigned>((n + kReduceThreads - 1) / kReduceThreads);
+  if (a.gated)
+    linear_reduce_kernel<AT, true><<<grid, kReduceThreads, 0, s>>>(a);
+  else
+    linear_reduce_kernel<AT, false><<<grid, kReduceThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename WT, class G>
 static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
   const int tn = a.gated ? G::TN / 2 : G::TN;
@@ -933,9 +1160,95 @@ static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------ choice of kernel
+//
+// More than 16 tokens: the tile and the number of K ranges with the least
+// estimated time.  A workgroup's K stage takes what its loads take (a part
+// that does not depend on the size and about 60 GB/s per compute unit,
+// shared by the workgroups on it) or what its MFMAs take; workgroups run in
+// rounds of as many as a compute unit's LDS holds.  Split sums are written
+// and read once more.  The constants were fitted to the tiles' times alone
+// and side by side (one workgroup per unit: 128 x 128 0.81 us a stage, 64 x 64
+// 0.54; the 256 x 256 tile 1.08); over 17..1024 tokens x 512..28672 rows x
+// 512..4096 K the choice measured within 12% of the best.
+
+enum LinearTile { kTileStream, kTile256, kTile128, kTile128Pair, kTile128x64, kTile128x64Pair,
+                  kTile64, kTileStaged128, kTileStaged64 };
+
+struct TileCost {
+  int tile, rows, tokens;
+  int lds_kb[2];  // stages in LDS: with weights of two or four bytes, of one
+  float fixed;    // us per stage apart from the bytes
+  float start;    // us per workgroup: first loads and epilogue
+};
+// the aligned tiles, then the staged ones
+constexpr TileCost kTileCosts[] = {
+    {kTile256, 256, 256, {160, 128}, 0.27f, 11.f},
+    {kTile128, 128, 128, {128, 96}, 0.27f, 1.f},
+    {kTile128Pair, 128, 128, {64, 48}, 0.27f, 1.f},
+    {kTile128x64, 128, 64, {96, 64}, 0.27f, 1.f},
+    {kTile128x64Pair, 128, 64, {72, 48}, 0.27f, 1.f},
+    {kTile64, 64, 64, {64, 48}, 0.25f, 0.5f},
+    {kTileStaged128, 128, 128, {32, 24}, 1.2f, 1.f},
+    {kTileStaged64, 64, 64, {16, 12}, 0.7f, 1.f},
+};
+constexpr int kComputeUnits = 256;
+constexpr float kUsPerKb = 0.017f;
+
+static bool linear_aligned(const LinearArgs& a) {
+  const int esz = a.w_dtype == kDtypeE4M3FN ? 16 : a.w_dtype == kDtypeBF16 ? 8 : 4;
+  const int xsz = a.act_dtype == kDtypeF32 ? 4 : 8;
+  return a.ldw % esz == 0 && a.ldx % xsz == 0 && a.K % esz == 0;
+}
+
 void linear_plan(LinearArgs* a) {
   a->splits = 1;
   a->ksplit = a->K;
+  a->tile = kTileStream;
+  if (a->M <= kLinStreamTokens) return;
+  const bool aligned = linear_aligned(*a);
+  const int wb = a->w_dtype == kDtypeE4M3FN ? 1 : a->w_dtype == kDtypeBF16 ? 2 : 4;
+  const int kc = wb == 4 ? 32 : 64;
+  const float bytes = static_cast<float>(a->R) * a->K * wb +
+                      static_cast<float>(a->M) * (a->K + a->N) * (wb == 4 ? 4 : 2);
+  float best = 1e30f;
+  for (const TileCost& t : kTileCosts) {
+    if (aligned != (t.tile < kTileStaged128)) continue;
+    const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) *
+                          ((a->R + t.rows - 1) / t.rows);
+    const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
+    // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
+    const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f * 1.1f;
+    const int waves = t.tile == kTile64 || t.tile == kTileStaged64 ? 4 : 8;
+    int held = 160 / t.lds_kb[wb == 1];
+    if (held > 16 / waves) held = 16 / waves;
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      // ranges of whole stage pairs, of at least four stages
+      const int per = ((a->K + want - 1) / want + 2 * kc - 1) / (2 * kc) * (2 * kc);
+      if (want > 1 && per < 4 * kc) break;
+      const int splits = (a->K + per - 1) / per;
+      const float stages = static_cast<float>((per + kc - 1) / kc);
+      int64_t left = (tiles * splits + kComputeUnits - 1) / kComputeUnits;  // per unit
+      const int64_t rounds = left / held;
+      auto round_us = [&](int n) {
+        float stage = t.fixed + kUsPerKb * kb;
+        if (n * kUsPerKb * kb > stage) stage = n * kUsPerKb * kb;
+        if (n * mfma > stage) stage = n * mfma;
+        return stages * stage + t.start;
+      };
+      float us = rounds * round_us(held);
+      if (left % held) us += round_us(static_cast<int>(left % held));
+      if (us < bytes / 4.7e6f) us = bytes / 4.7e6f;
+      if (splits > 1)
+        us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 5.2e6f;
+      if (us < best) {
+        best = us;
+        a->tile = t.tile;
+        a->splits = splits;
+        a->ksplit = splits > 1 ? per : a->K;
+      }
+    }
+  }
 }
 
 size_t linear_part_bytes(const LinearArgs& a) {
@@ -944,11 +1257,22 @@ size_t linear_part_bytes(const LinearArgs& a) {
 
 template <typename WT>
 static hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
-  if (a.M <= kLinStreamTokens) return launch_stream<WT>(a, s);
-  constexpr int esz = 16 / (int)sizeof(WT), xsz = 16 / (int)sizeof(typename StreamGeom<WT>::AT);
-  const bool aligned = a.ldw % esz == 0 && a.ldx % xsz == 0 && a.K % esz == 0;
-  if (aligned && a.M >= 128) return launch_pp<WT>(a, s);
-  return launch_staged<WT, LinGeom<WT, 2, 2, 2, 2>>(a, s);
+  hipError_t e = hipErrorInvalidValue;
+  switch (a.tile) {
+    case kTileStream: return launch_stream<WT>(a, s);
+    case kTile256: e = launch_pp<WT>(a, s); break;
+    // a ring of four stages alone on its compute unit, or less LDS and two
+    // workgroups side by side
+    case kTile128: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 4>(a, s); break;
+    case kTile128Pair: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 2>(a, s); break;
+    case kTile128x64: e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 4>(a, s); break;
+    case kTile128x64Pair: e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 3>(a, s); break;
+    case kTile64: e = launch_tile<WT, LinGeom<WT, 2, 2, 2, 2>, 4>(a, s); break;
+    case kTileStaged128: e = launch_staged<WT, LinGeom<WT, 2, 4, 4, 2>>(a, s); break;
+    case kTileStaged64: e = launch_staged<WT, LinGeom<WT, 2, 2, 2, 2>>(a, s); break;
+  }
+  if (e == hipSuccess && a.part) e = launch_reduce<typename StreamTypes<WT>::AT>(a, s);
+  return e;
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
