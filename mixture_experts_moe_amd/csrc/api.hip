@@ -937,14 +937,14 @@ MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate,
   a.res = residual;
   a.out = out;
   a.logits = reinterpret_cast<float*>(ws + p.logits);
-  a.flags = reinterpret_cast<int32_t*>(ws + p.flags);
+  a.flags = reinterpret_cast<uint8_t*>(ws + p.flags);
   a.h = ws + p.h;
   a.T = static_cast<int>(desc->num_tokens);
   a.d = static_cast<int>(desc->hidden);
   a.E = static_cast<int>(desc->num_experts);
   a.I = static_cast<int>(desc->intermediate);
   a.k = top_k;
-  a.wgs = moe::decode_workgroups(a.T, cus);
+  a.wgs = moe::decode_workgroups(cus);
   a.wait_limit = desc->schedule == MOE_SCHED_QUEUE ? 0 : kDecodeWaitTicks;
   hipError_t e =
       timed(MOE_KERNEL_ROUTE_LOGITS, s, [&] { return moe::launch_decode_route(a, s); });

@@ -28,6 +28,12 @@ constexpr int kDecThreads = 512;
 constexpr int kDecWaves = kDecThreads / 64;
 constexpr int kDecMaxRows = kDecodeMaxTokens * kMaxTopK;  // slots
 constexpr int kDecMaxWgs = 1024;
+constexpr int kDecGroup = 32;                        // workgroups of a group
+constexpr int kDecGroups = kDecMaxWgs / kDecGroup;
+constexpr int kDecLine = 128;
+// a byte per workgroup, then lines: the groups' counters, their go words, the
+// counter of groups
+constexpr int kDecFlagBytes = kDecMaxWgs + (2 * kDecGroups + 1) * kDecLine;
 
 // A value that every lane holds alike, as a scalar: addresses built from it
 // stay in scalar registers.
@@ -37,64 +43,55 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 
 constexpr int kRouteThreads = 256;
 
-// EP experts per workgroup, TT >= T tokens; a thread takes every 256th unit
-// of four K.
-template <typename AT, int EP, int TT>
+// One expert and up to kRouteTokens tokens per workgroup; a thread takes every
+// 256th unit of four K.
+constexpr int kRouteTokens = 4;
+template <typename AT>
 __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(
     const AT* __restrict__ x, const float* __restrict__ w_gate, float* __restrict__ logits,
-    int32_t* __restrict__ flags, int nflags, int T, int E, int d) {
-  __shared__ float part[kRouteThreads / 64][EP * TT];
+    uint8_t* __restrict__ flags, int T, int E, int d) {
+  __shared__ float part[kRouteThreads / 64][kRouteTokens];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int e0 = blockIdx.x * EP;
-  if (blockIdx.x == 0)
-    for (int i = tid; i < nflags; i += kRouteThreads) flags[i] = 0;
-  float acc[EP][TT];
-#pragma unroll
-  for (int e = 0; e < EP; ++e)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[e][t] = 0.f;
+  const int e = blockIdx.x, t0 = blockIdx.y * kRouteTokens;
+  const int n = min(T - t0, kRouteTokens);
+  if (e == 0 && t0 == 0)
+    for (int i = tid; i < kDecFlagBytes / 4; i += kRouteThreads)
+      reinterpret_cast<uint32_t*>(flags)[i] = 0;
+  x += static_cast<size_t>(t0) * d;
+  w_gate += static_cast<size_t>(e) * d;
+  float acc[kRouteTokens] = {};
   for (int u = tid; u < d / 4; u += kRouteThreads) {
-    float4 w[EP];
+    const float4 w = *reinterpret_cast<const float4*>(w_gate + 4 * u);
 #pragma unroll
-    for (int e = 0; e < EP; ++e)
-      w[e] = *reinterpret_cast<const float4*>(
-          w_gate + static_cast<size_t>(min(e0 + e, E - 1)) * d + 4 * u);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      if (t < T) {
-        float v[4];
-        if constexpr (sizeof(AT) == 4) {
-          const float4 q = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * d + 4 * u);
-          v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(x + static_cast<size_t>(t) * d + 4 * u);
-          v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
-          v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
-        }
-#pragma unroll
-        for (int e = 0; e < EP; ++e) {
-          acc[e][t] = fmaf(w[e].x, v[0], acc[e][t]);
-          acc[e][t] = fmaf(w[e].y, v[1], acc[e][t]);
-          acc[e][t] = fmaf(w[e].z, v[2], acc[e][t]);
-          acc[e][t] = fmaf(w[e].w, v[3], acc[e][t]);
-        }
+    for (int t = 0; t < kRouteTokens; ++t) {
+      // tokens past the last repeat it
+      const AT* row = x + static_cast<size_t>(min(t, n - 1)) * d + 4 * u;
+      float v[4];
+      if constexpr (sizeof(AT) == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(row);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(row);
+        v[0] = __uint_as_float(q.x << 16), v[1] = __uint_as_float(q.x & 0xffff0000u);
+        v[2] = __uint_as_float(q.y << 16), v[3] = __uint_as_float(q.y & 0xffff0000u);
       }
+      acc[t] = fmaf(w.x, v[0], acc[t]);
+      acc[t] = fmaf(w.y, v[1], acc[t]);
+      acc[t] = fmaf(w.z, v[2], acc[t]);
+      acc[t] = fmaf(w.w, v[3], acc[t]);
     }
   }
 #pragma unroll
-  for (int e = 0; e < EP; ++e)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const float v = wave_sum(acc[e][t]);
-      if (lane == 0) part[wave][e * TT + t] = v;
-    }
+  for (int t = 0; t < kRouteTokens; ++t) {
+    const float v = wave_sum(acc[t]);
+    if (lane == 0) part[wave][t] = v;
+  }
   __syncthreads();
-  if (tid < EP * TT) {
+  if (tid < n) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kRouteThreads / 64; ++w) v += part[w][tid];
-    const int e = e0 + tid / TT, t = tid % TT;
-    if (e < E && t < T) logits[static_cast<size_t>(t) * E + e] = v;
+    logits[static_cast<size_t>(t0 + tid) * E + e] = v;
   }
 }
 
@@ -243,63 +240,79 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
 // ------------------------------------------------------------ the layer
 
 
-template <typename WT, int TQ>
+// kMany: more than four tokens in the call; experts with up to four of them
+// take the 4x4 MFMAs, the others the 16x16 (stream.h).
+template <typename WT, bool kMany>
 struct DecLayer {
   using G = StreamGeom<WT>;
   using AT = typename G::AT;
+  template <bool kHalf>
+  using S16 = Stream16<WT, 1, true, kHalf>;
+  static constexpr int kTok = kMany ? 16 : 4;  // token columns of an expert
+  // chunks of 16 rows in flight per wave (e4m3fn tokens take twice the registers)
+  static constexpr int kBatch = sizeof(WT) == 1 ? 2 : 4;
   const DecodeArgs& a;
   DecSel& sel;
-  float (*red)[kDecodeMaxTokens][16];  // [2 * kDecWaves]: sums of 16 rows per token and wave
+  float (*red)[kTok][16];  // [2 * kDecWaves]: sums of 16 rows per token and wave
+  uint8_t* lds;            // this wave's weights (kMany)
 
   int lane, wave;
 
-  // Token rows of quad t of an expert with n rows from `base`; columns past
-  // the last repeat it (never stored).
-  template <int NQ, int RQ>
-  __device__ __forceinline__ void tokens(Stream<WT, RQ, NQ, true>& st, const AT* m, int ld,
-                                         int base, int n, bool h_rows) const {
-    const int unit = lane / 4 * (G::kLaneK * (int)sizeof(AT));
-    st.xb = reinterpret_cast<const uint8_t*>(m + (h_rows ? static_cast<size_t>(base) * ld : 0));
-#pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      const int j = min(4 * t + (lane & 3), n - 1);
-      const int row = h_rows ? j : sel.token[base + j];
-      st.xo[t] = static_cast<uint32_t>(row) * ld * sizeof(AT) + unit;
-    }
+  // The lane's token row (of n rows from `base`; columns past the last repeat
+  // it, never stored): wave-uniform base and byte offset.
+  __device__ __forceinline__ void token(const AT* m, int ld, int base, int n, int col, bool h_rows,
+                                        const uint8_t** xb, uint32_t* xo) const {
+    *xb = reinterpret_cast<const uint8_t*>(m + (h_rows ? static_cast<size_t>(base) * ld : 0));
+    const int j = min(col, n - 1);
+    *xo = static_cast<uint32_t>(h_rows ? j : sel.token[base + j]) * ld * sizeof(AT);
   }
 
-  // ---- W13: 8 channels (two gate quads, the matching up quads) from c0 of
-  // selected expert i, K split `sub` of `S`; sums to red[slot].
-  template <int NQ>
+  // ---- W13: 8 channels (gate rows, the matching up rows) from c0 of selected
+  // expert i, K split `sub` of `S`; sums to red[slot]: 8 gate, 8 up.
   __device__ __forceinline__ void w13_group(int i, int c0, int sub, int S, int slot) const {
     const int e = uniform(sel.expert[i]), base = uniform(sel.base[i]);
     const int n = uniform(sel.base[i + 1]) - base;
-    Stream<WT, 4, NQ, true> st;
     const size_t ldb = static_cast<size_t>(a.d) * sizeof(WT);
-    const uint8_t* w = static_cast<const uint8_t*>(a.w13) + static_cast<size_t>(e) * 2 * a.I * ldb;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      st.wq[q] = w + static_cast<size_t>((q >> 1) * a.I + c0 + 4 * (q & 1)) * ldb;
-      st.wo[q] = static_cast<uint32_t>((lane & 3) * ldb) + 16 * (lane >> 2);
-    }
-    tokens<NQ, 4>(st, static_cast<const AT*>(a.x), a.d, base, n, false);
-    f32x4 acc[4][NQ];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int t = 0; t < NQ; ++t) acc[q][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint8_t* gate = static_cast<const uint8_t*>(a.w13) +
+                          (static_cast<size_t>(e) * 2 * a.I + c0) * ldb;
+    const uint8_t* up = gate + a.I * ldb;
     const int full = a.d / G::kChunk, left = a.d % G::kChunk;
     const int mine = full > sub ? (full - sub + S - 1) / S : 0;
-    st.template run<NQ == 1 ? 4 : 2>(sub, mine, S, acc);
-    if (left && full % S == sub) st.tail(full, left, acc);
+    const bool last = left && full % S == sub;
+    if (kMany && n > 4) {
+      S16<false> st;
+      st.wq[0][0] = gate;
+      st.wq[0][1] = up;
+      auto row_off = [&](int, int r) { return static_cast<uint32_t>((r & 7) * ldb); };
+      st.place(0, [&](int r) { return row_off(0, r); });
+      st.lds = lds;
+      token(static_cast<const AT*>(a.x), a.d, base, n, lane & 15, false, &st.xb, &st.xo);
+      st.xo += (lane >> 4) * (G::kLaneK * sizeof(AT));
+      f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+      st.run(sub, mine, S, acc);
+      if (last) st.tail(full, left, row_off, acc);
+      *reinterpret_cast<f32x4*>(&red[slot][(lane & 15) % kTok][4 * (lane >> 4)]) = acc[0];
+      return;
+    }
+    Stream<WT, 4, 1, true> st;
 #pragma unroll
-    for (int t = 0; t < NQ; ++t)
+    for (int q = 0; q < 4; ++q)
+      st.place(q, [&](int r) { return static_cast<uint32_t>((4 * (q & 1) + r) * ldb); });
+    st.wq[0] = gate;
+    st.wq[1] = up;
+    token(static_cast<const AT*>(a.x), a.d, base, n, lane & 3, false, &st.xb, &st.xo[0]);
+    st.xo[0] += (lane >> 2) * (G::kLaneK * sizeof(AT));
+    f32x4 acc[4][1];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 4; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.template run<kBatch>(sub, mine, S, acc);
+    if (last) st.tail(full, left, acc);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[q][t][v] = stream_wave_sum(acc[q][t][v]);
-        if (lane < 4) *reinterpret_cast<f32x4*>(&red[slot][4 * t + lane][4 * q]) = acc[q][t];
-      }
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[q][0][v] = stream_wave_sum(acc[q][0][v]);
+      if (lane < 4) *reinterpret_cast<f32x4*>(&red[slot][lane][4 * q]) = acc[q][0];
+    }
   }
 
   // K ranges per group so that the workgroup's waves finish together: the
@@ -330,20 +343,11 @@ struct DecLayer {
     const int sub = wave % S, gsel = wave / S;
     int buf = 0;
     for (int g = g0; g < g1; g += at_once, buf ^= kDecWaves) {
-      if (g + gsel < g1) {
-        const int i = (g + gsel) / per, c0 = 8 * ((g + gsel) % per);
-        const int n = uniform(sel.base[i + 1] - sel.base[i]);
-        if (TQ == 1 || n <= 4)
-          w13_group<1>(i, c0, sub, S, buf + wave);
-        else if (TQ == 2 || n <= 8)
-          w13_group<TQ >= 2 ? 2 : 1>(i, c0, sub, S, buf + wave);
-        else
-          w13_group<TQ>(i, c0, sub, S, buf + wave);
-      }
+      if (g + gsel < g1) w13_group((g + gsel) / per, 8 * ((g + gsel) % per), sub, S, buf + wave);
       __syncthreads();
       // channel pair cp of token column j of group gs
-      for (int o = threadIdx.x; o < at_once * 4 * TQ * 4; o += kDecThreads) {
-        const int cp = o & 3, j = (o >> 2) % (4 * TQ), gs = (o >> 2) / (4 * TQ);
+      for (int o = threadIdx.x; o < at_once * kTok * 4; o += kDecThreads) {
+        const int cp = o & 3, j = (o >> 2) % kTok, gs = (o >> 2) / kTok;
         if (g + gs >= g1) continue;
         const int i = (g + gs) / per, c = 8 * ((g + gs) % per) + 2 * cp;
         const int base = sel.base[i];
@@ -382,49 +386,60 @@ struct DecLayer {
 
   // ---- W2: output rows r0 .. r0+4*RQ-1.
 
+  // four rows' sums v of one expert for token column j, into the wave's out sums
+  __device__ __forceinline__ void add(int e, int base, int j, int r0, int r, f32x4 v) const {
+    const float gate = sel.gate[base + j];
+    float* o = &red[wave][sel.token[base + j]][r];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(WT) == 1)
+        v[i] *= a.s2[a.scale_mode == kScaleChannel ? static_cast<size_t>(e) * a.d + r0 + r + i : e];
+      o[i] += gate * v[i];
+    }
+  }
+
   // chunks [c0, c1) of selected expert i (the last may be partial); adds the
   // expert's gated, scaled sums to the wave's out sums
-  template <int NQ, int RQ>
+  template <int RQ>
   __device__ __forceinline__ void w2_part(int i, int r0, int c0, int c1) const {
     const int e = uniform(sel.expert[i]), base = uniform(sel.base[i]);
     const int n = uniform(sel.base[i + 1]) - base;
-    Stream<WT, RQ, NQ, true> st;
     const size_t ldb = static_cast<size_t>(a.I) * sizeof(WT);
     const uint8_t* w = static_cast<const uint8_t*>(a.w2) + (static_cast<size_t>(e) * a.d + r0) * ldb;
-#pragma unroll
-    for (int q = 0; q < RQ; ++q) {
-      st.wq[q] = w + 4 * q * ldb;
-      st.wo[q] = static_cast<uint32_t>((lane & 3) * ldb) + 16 * (lane >> 2);
+    const int full = a.I / G::kChunk, left = a.I % G::kChunk;
+    if (kMany && n > 4) {
+      S16<RQ == 2> st;
+      st.wq[0][0] = w;
+      st.wq[0][1] = w + 8 * ldb;
+      auto row_off = [&](int, int r) { return static_cast<uint32_t>((r & 7) * ldb); };
+      st.place(0, [&](int r) { return row_off(0, r); });
+      st.lds = lds;
+      token(static_cast<const AT*>(a.h), a.I, base, n, lane & 15, true, &st.xb, &st.xo);
+      st.xo += (lane >> 4) * (G::kLaneK * sizeof(AT));
+      f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
+      st.run(c0, min(c1, full) - c0, 1, acc);
+      if (c1 > full) st.tail(full, left, row_off, acc);
+      const int j = lane & 15, r = 4 * (lane >> 4);
+      if (j < n && r < 4 * RQ) add(e, base, j, r0, r, acc[0]);
+      return;
     }
-    tokens<NQ, RQ>(st, static_cast<const AT*>(a.h), a.I, base, n, true);
-    f32x4 acc[RQ][NQ];
+    Stream<WT, RQ, 1, true> st;
 #pragma unroll
     for (int q = 0; q < RQ; ++q)
+      st.place(q, [&](int r) { return static_cast<uint32_t>((4 * q + r) * ldb); });
+    st.wq[0] = st.wq[1] = w;
+    token(static_cast<const AT*>(a.h), a.I, base, n, lane & 3, true, &st.xb, &st.xo[0]);
+    st.xo[0] += (lane >> 2) * (G::kLaneK * sizeof(AT));
+    f32x4 acc[RQ][1];
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) acc[q][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int full = a.I / G::kChunk, left = a.I % G::kChunk;
-    st.template run<NQ == 1 ? 4 : 2>(c0, min(c1, full) - c0, 1, acc);
+    for (int q = 0; q < RQ; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    st.template run<RQ == 2 ? 2 * kBatch : kBatch>(c0, min(c1, full) - c0, 1, acc);
     if (c1 > full) st.tail(full, left, acc);
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) {
-      const int j = 4 * t + (lane & 3);
-      const float gate = j < n ? sel.gate[base + j] : 0.f;
+    for (int q = 0; q < RQ; ++q) {
 #pragma unroll
-      for (int q = 0; q < RQ; ++q) {
-        f32x4 s;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          s[v] = stream_wave_sum(acc[q][t][v]);
-          if (sizeof(WT) == 1)
-            s[v] *= a.s2[a.scale_mode == kScaleChannel
-                             ? static_cast<size_t>(e) * a.d + r0 + 4 * q + v : e];
-        }
-        if (lane < 4 && j < n) {
-          float* o = &red[wave][sel.token[base + j]][4 * q];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) o[v] += gate * s[v];
-        }
-      }
+      for (int v = 0; v < 4; ++v) acc[q][0][v] = stream_wave_sum(acc[q][0][v]);
+      if (lane < n) add(e, base, lane, r0, 4 * q, acc[q][0]);
     }
   }
 
@@ -432,7 +447,7 @@ struct DecLayer {
   __device__ __forceinline__ void w2_rows(int r0) const {
     const int tid = threadIdx.x;
     __syncthreads();  // the sums before have been read
-    for (int o = tid; o < kDecWaves * kDecodeMaxTokens * 16; o += kDecThreads)
+    for (int o = tid; o < kDecWaves * kTok * 16; o += kDecThreads)
       (&red[0][0][0])[o] = 0.f;
     __syncthreads();
     // the waves share the (expert, chunk) list evenly
@@ -442,13 +457,7 @@ struct DecLayer {
     for (int it = i0; it < i1;) {
       const int i = it / C, c0 = it % C;
       const int c1 = min(C, c0 + i1 - it);
-      const int n = uniform(sel.base[i + 1] - sel.base[i]);
-      if (TQ == 1 || n <= 4)
-        w2_part<1, RQ>(i, r0, c0, c1);
-      else if (TQ == 2 || n <= 8)
-        w2_part<TQ >= 2 ? 2 : 1, RQ>(i, r0, c0, c1);
-      else
-        w2_part<TQ, RQ>(i, r0, c0, c1);
+      w2_part<RQ>(i, r0, c0, c1);
       it += c1 - c0;
     }
     __syncthreads();
@@ -477,38 +486,69 @@ struct DecLayer {
   }
 };
 
+// The meeting between the halves.  A workgroup that has written its share sets
+// its flag and counts itself on its group's counter (every counter and go
+// word in a 128-byte line of its own: hundreds of workgroups polling or adding
+// to one line cost tens of microseconds); the last of a group counts the
+// group, the last group writes every group's go word, and a workgroup polls
+// only that of its own group.  The flags are read only by a workgroup that
+// has waited too long.
+
 // Share b is out (every thread's stores of it are complete before the barrier).
-__device__ __forceinline__ void dec_publish(int32_t* flags, int b) {
+__device__ __forceinline__ void dec_publish(uint8_t* flags, int b) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) __hip_atomic_store(flags + b, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0)
+    __hip_atomic_store(flags + b, uint8_t(1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Counts the workgroup (once, after publishing its own share).
+__device__ __forceinline__ void dec_arrive(const DecodeArgs& a) {
+  if (threadIdx.x != 0) return;
+  int32_t* words = reinterpret_cast<int32_t*>(a.flags + kDecMaxWgs);
+  auto line = [&](int i) { return words + i * (kDecLine / 4); };
+  const int groups = (a.wgs + kDecGroup - 1) / kDecGroup;
+  const int g = blockIdx.x / kDecGroup;
+  const int members = min(kDecGroup, a.wgs - g * kDecGroup);
+  if (__hip_atomic_fetch_add(line(g), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != members - 1)
+    return;
+  if (__hip_atomic_fetch_add(line(2 * kDecGroups), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) !=
+      groups - 1)
+    return;
+  for (int i = 0; i < groups; ++i)
+    __hip_atomic_store(line(kDecGroups + i), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Waits until every share is out (-1), or until `limit` ticks of the 100 MHz
-// clock have passed: then one that is missing, the first from the caller's
-// own index on.
-__device__ __forceinline__ int dec_wait(const int32_t* flags, int wgs, int64_t limit, int* lds) {
+// clock have passed: then one whose flag is missing, the first from the
+// caller's own index on.
+__device__ __forceinline__ int dec_wait(const DecodeArgs& a, int64_t limit, int* lds) {
+  constexpr int kNone = 1 << 30;
   if (threadIdx.x < 64) {
     const int lane = threadIdx.x;
+    const int32_t* go = reinterpret_cast<const int32_t*>(a.flags + kDecMaxWgs) +
+                        (kDecGroups + blockIdx.x / kDecGroup) * (kDecLine / 4);
     const int64_t start = wall_clock64();
-    int found;
-    for (;;) {
-      int after = 1 << 30, any = 1 << 30;  // lowest missing index: from blockIdx on, of all
-      for (int i = lane; i < wgs; i += 64)
-        if (!__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) {
-          any = min(any, i);
-          if (i >= static_cast<int>(blockIdx.x)) after = min(after, i);
-        }
+    int found = kNone;
+    while (!uniform(__hip_atomic_load(go, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))) {
+      if (wall_clock64() - start >= limit) {
+        int after = kNone, any = kNone;  // lowest missing: from blockIdx on, of all
+        for (int b = lane; b < a.wgs; b += 64)
+          if (!__hip_atomic_load(a.flags + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) {
+            any = min(any, b);
+            if (b >= static_cast<int>(blockIdx.x)) after = min(after, b);
+          }
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        any = min(any, __shfl_xor(any, off, 64));
-        after = min(after, __shfl_xor(after, off, 64));
+        for (int off = 32; off > 0; off >>= 1) {
+          any = min(any, __shfl_xor(any, off, 64));
+          after = min(after, __shfl_xor(after, off, 64));
+        }
+        found = after < kNone ? after : any;
+        break;
       }
-      found = __builtin_amdgcn_readfirstlane(after < (1 << 30) ? after : any);
-      if (found == 1 << 30 || wall_clock64() - start >= limit) break;
-      __builtin_amdgcn_s_sleep(2);
+      __builtin_amdgcn_s_sleep(1);
     }
-    if (lane == 0) *lds = found == 1 << 30 ? -1 : found;
+    if (lane == 0) *lds = found == kNone ? -1 : found;
   }
   __syncthreads();
   const int b = uniform(*lds);
@@ -516,22 +556,26 @@ __device__ __forceinline__ int dec_wait(const int32_t* flags, int wgs, int64_t l
   return b;
 }
 
-template <typename WT, int TQ>
-__global__ __launch_bounds__(kDecThreads, TQ == 1 ? 4 : 2) void decode_layer_kernel(DecodeArgs a,
-                                                                                   int phases) {
+template <typename WT, bool kMany>
+__global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs a, int phases) {
+  using Layer = DecLayer<WT, kMany>;
   __shared__ DecSel sel;
-  __shared__ __attribute__((aligned(16))) float red[2 * kDecWaves][kDecodeMaxTokens][16];
+  __shared__ __attribute__((aligned(16))) float red[2 * kDecWaves][Layer::kTok][16];
+  __shared__ __attribute__((aligned(1024))) uint8_t weights[kMany ? kDecWaves : 1]
+                                                           [kMany ? 4096 : 16];
   __shared__ int next;
   dec_select(a.logits, a.T, a.E, a.k, sel);
-  const DecLayer<WT, TQ> layer{a, sel, red, static_cast<int>(threadIdx.x & 63),
-                               static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))};
+  const int wave = static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  const Layer layer{a, sel, red, weights[kMany ? wave : 0], static_cast<int>(threadIdx.x & 63), wave};
   if (phases & 1) {
     int64_t limit = a.wait_limit;
-    for (int b = blockIdx.x; b >= 0; limit = 0) {  // b is wave-uniform
+    for (int b = blockIdx.x; b >= 0;) {  // b is wave-uniform
       layer.w13_share(b);
       if (!(phases & 2)) return;
       dec_publish(a.flags, b);
-      b = dec_wait(a.flags, a.wgs, limit, &next);
+      if (b == static_cast<int>(blockIdx.x)) dec_arrive(a);
+      b = dec_wait(a, limit, &next);
+      limit = 0;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // h as the others wrote it
   }
@@ -540,28 +584,16 @@ __global__ __launch_bounds__(kDecThreads, TQ == 1 ? 4 : 2) void decode_layer_ker
 
 // ------------------------------------------------------------ launchers
 
-static int decode_quads(int T) { return T <= 4 ? 1 : T <= 8 ? 2 : 4; }
+// As many workgroups as are resident at once: two of eight waves per unit.
+int decode_workgroups(int cus) { return 2 * cus < kDecMaxWgs ? 2 * cus : kDecMaxWgs; }
 
-int decode_workgroups(int T, int cus) {
-  const int n = decode_quads(T) == 1 ? 2 * cus : cus;  // as many as are resident at once
-  return n < kDecMaxWgs ? n : kDecMaxWgs;
-}
-
-size_t decode_flag_bytes() { return kDecMaxWgs * sizeof(int32_t); }
-
-template <typename AT, int TT>
-static void route(const DecodeArgs& a, hipStream_t s) {
-  constexpr int EP = 1;
-  decode_route_kernel<AT, EP, TT><<<(a.E + EP - 1) / EP, kRouteThreads, 0, s>>>(
-      static_cast<const AT*>(a.x), a.w_gate, a.logits, a.flags, a.wgs, a.T, a.E, a.d);
-}
+size_t decode_flag_bytes() { return kDecFlagBytes; }
 
 template <typename AT>
 static hipError_t route(const DecodeArgs& a, hipStream_t s) {
-  if (a.T <= 4)
-    route<AT, 4>(a, s);
-  else
-    route<AT, 16>(a, s);
+  const dim3 grid(a.E, (a.T + kRouteTokens - 1) / kRouteTokens);
+  decode_route_kernel<AT><<<grid, kRouteThreads, 0, s>>>(static_cast<const AT*>(a.x), a.w_gate,
+                                                         a.logits, a.flags, a.T, a.E, a.d);
   return hipGetLastError();
 }
 
@@ -571,11 +603,10 @@ hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s) {
 
 template <typename WT>
 static hipError_t layer(const DecodeArgs& a, int phases, hipStream_t s) {
-  switch (decode_quads(a.T)) {
-    case 1: decode_layer_kernel<WT, 1><<<a.wgs, kDecThreads, 0, s>>>(a, phases); break;
-    case 2: decode_layer_kernel<WT, 2><<<a.wgs, kDecThreads, 0, s>>>(a, phases); break;
-    default: decode_layer_kernel<WT, 4><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
-  }
+  if (a.T <= 4)
+    decode_layer_kernel<WT, false><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
+  else
+    decode_layer_kernel<WT, true><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
   return hipGetLastError();
 }
 

@@ -268,14 +268,14 @@ struct DecodeArgs {
   void* out;            // [T, d]
   float* logits;        // [T, E] (workspace)
   void* h;              // [T*k, I] act dtype (workspace)
-  int32_t* flags;       // decode_flag_bytes() (workspace), cleared by the route launch
+  uint8_t* flags;       // decode_flag_bytes() (workspace), cleared by the route launch
   int T, d, E, I, k;
   int wgs;              // workgroups of the layer launch
   int64_t wait_limit;   // 100 MHz ticks before a workgroup computes a missing share itself
 };
 
-// Workgroups that `cus` compute units hold at once, for T tokens.
-int decode_workgroups(int T, int cus);
+// Workgroups of the layer launch that `cus` compute units hold at once.
+int decode_workgroups(int cus);
 size_t decode_flag_bytes();
 hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s);
 // phases: 1 = W13, 2 = W2 and the sum over experts, 3 = both in one launch.

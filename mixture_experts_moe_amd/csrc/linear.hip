@@ -1018,10 +1018,11 @@ __global__ __launch_bounds__(kLinStreamThreads, 4) void linear_stream_kernel(Lin
     Stream<WT, 4 * RT, 1, kAligned> st;
 #pragma unroll
     for (int q = 0; q < 4 * RT; ++q) {
-      const int c = 4 * q % kCh;
-      st.wq[q] = first(c, 4 * q >= kCh);
-      st.wo[q] = offset(c, lane & 3) + 16 * (lane >> 2);
+      const int r = 4 * q % (kRows / 2);  // its first row in its half
+      st.place(q, [&](int i) { return offset(q < 2 * RT || kGated ? 0 : kRows / 2, r + i); });
     }
+    st.wq[0] = first(0, false);
+    st.wq[1] = first(kGated ? 0 : kRows / 2, kGated);
     st.xb = static_cast<const uint8_t*>(a.x);
     st.xo[0] = static_cast<uint32_t>(min(lane & 3, M - 1) * a.ldx * sizeof(AT)) +
                (lane >> 2) * (G::kLaneK * sizeof(AT));

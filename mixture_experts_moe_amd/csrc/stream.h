@@ -89,8 +89,9 @@ __device__ __forceinline__ void stream_mma(const u32x4 (&w)[RQ], const StreamTok
   }
 }
 
-// The operand rows.  Weight quad q: wq[q] (wave-uniform) + wo[q] (this lane's
-// row and K unit, bytes); token quad t: xb (wave-uniform) + xo[t] (this
+// The operand rows.  Weight quad q: wq[0] for the first half of the quads,
+// wq[1] for the second (wave-uniform) + wo[q] (this lane's row and K unit,
+// bytes); token quad t: xb (wave-uniform) + xo[t] (this
 // lane's token row and K unit; columns past the last token repeat it and are
 // dropped).
 //
@@ -100,10 +101,18 @@ template <typename WT, int RQ, int TQ, bool kAligned>
 struct Stream {
   using G = StreamGeom<WT>;
   using AT = typename G::AT;
-  const uint8_t* wq[RQ];
+  const uint8_t* wq[2];
   uint32_t wo[RQ];
   const uint8_t* xb;
   uint32_t xo[TQ];
+
+  // quad q's rows: row_off(r) = bytes from its half's base to row r of the quad
+  template <class F>
+  __device__ __forceinline__ void place(int q, F row_off) {
+    const int lane = threadIdx.x & 63;
+    wo[q] = row_off(lane & 3) + 16 * (lane >> 2);
+  }
+  __device__ __forceinline__ const uint8_t* base(int q) const { return wq[RQ > 1 && q >= RQ / 2]; }
 
   static constexpr int kWStep = 256;                            // bytes per chunk
   static constexpr int kXStep = G::kChunk * (int)sizeof(AT);
@@ -118,7 +127,7 @@ struct Stream {
 #pragma unroll
       for (int q = 0; q < RQ; ++q)
         w[q] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(wq[q]), wo[q], chunk * kWStep,
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc(base(q)), wo[q], chunk * kWStep,
                                                          kNonTemporal));
 #pragma unroll
       for (int t = 0; t < TQ; ++t)
@@ -130,7 +139,7 @@ struct Stream {
     } else {
 #pragma unroll
       for (int q = 0; q < RQ; ++q)
-        w[q] = reinterpret_cast<const StreamUnit*>(wq[q] + static_cast<size_t>(chunk) * kWStep +
+        w[q] = reinterpret_cast<const StreamUnit*>(base(q) + static_cast<size_t>(chunk) * kWStep +
                                                    wo[q])
                    ->v;
 #pragma unroll
@@ -163,9 +172,17 @@ struct Stream {
   template <int P>
   __device__ __forceinline__ void run(int c0, int n, int step, f32x4 (&acc)[RQ][TQ]) const {
     for (; n >= P; n -= P, c0 += P * step) batch<P>(c0, step, acc);
-    if (P > 2 && n >= 2) {
-      batch<2>(c0, step, acc);
-      n -= 2, c0 += 2 * step;
+    if constexpr (P > 4) {
+      if (n >= 4) {
+        batch<4>(c0, step, acc);
+        n -= 4, c0 += 4 * step;
+      }
+    }
+    if constexpr (P > 2) {
+      if (n >= 2) {
+        batch<2>(c0, step, acc);
+        n -= 2, c0 += 2 * step;
+      }
     }
     if (n >= 1) batch<1>(c0, step, acc);
   }
@@ -177,7 +194,7 @@ struct Stream {
     StreamTok<WT, TQ> x;
 #pragma unroll
     for (int q = 0; q < RQ; ++q)
-      w[q] = part<WT>(wq[q] + static_cast<size_t>(chunk) * kWStep + wo[q], left - k);
+      w[q] = part<WT>(base(q) + static_cast<size_t>(chunk) * kWStep + wo[q], left - k);
 #pragma unroll
     for (int t = 0; t < TQ; ++t)
 #pragma unroll
