@@ -41,10 +41,10 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 
 // ------------------------------------------------------------ router logits
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 
 // One expert and up to kRouteTokens tokens per workgroup; a thread takes every
-// 256th unit of four K.
+// 512th unit of four K.
 constexpr int kRouteTokens = 4;
 template <typename AT>
 __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(
@@ -60,6 +60,7 @@ __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(
   x += static_cast<size_t>(t0) * d;
   w_gate += static_cast<size_t>(e) * d;
   float acc[kRouteTokens] = {};
+#pragma unroll 2
   for (int u = tid; u < d / 4; u += kRouteThreads) {
     const float4 w = *reinterpret_cast<const float4*>(w_gate + 4 * u);
 #pragma unroll
@@ -105,10 +106,14 @@ struct DecSel {
   uint16_t base[kMaxExperts + 1];
   uint8_t token[kDecMaxRows];
   float gate[kDecMaxRows];
-  uint16_t mask[kMaxExperts];  // tokens of each expert, while selecting
-  uint16_t slot_e[kDecMaxRows];
-  float slot_gate[kDecMaxRows];
   int n;  // experts selected
+};
+
+// Used while selecting only.
+struct DecScratch {
+  float slot_gate[kDecMaxRows];
+  uint32_t mask[kMaxExperts];  // bit t: token t selected this expert
+  uint16_t slot_e[kDecMaxRows];
 };
 
 // Order-preserving key: greater logit, greater key; NaN as -inf; both zeros
@@ -152,11 +157,9 @@ __device__ __forceinline__ void dec_topk(const float* row, int E, int k, uint16_
         best = key[i];
         bi = i;
       }
-    uint32_t m = best;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(m, off, 64)));
+    const uint32_t m = uniform(static_cast<int>(stream_wave_max(best)));
     const int src = __ffsll(static_cast<unsigned long long>(__ballot(best == m))) - 1;
-    const int e = __shfl(lane * per + bi, src, 64);
+    const int e = __builtin_amdgcn_readlane(lane * per + bi, src);
     if (lane == src) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
@@ -177,25 +180,21 @@ __device__ __forceinline__ void dec_topk(const float* row, int E, int k, uint16_
   }
 }
 
-__device__ __forceinline__ void dec_select(const float* logits, int T, int E, int k, DecSel& s) {
+__device__ __forceinline__ void dec_select(const float* logits, int T, int E, int k, DecSel& s,
+                                           DecScratch& w) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < E; e += kDecThreads) s.mask[e] = 0;
+  for (int e = tid; e < E; e += kDecThreads) w.mask[e] = 0;
   for (int t = wave; t < T; t += kDecWaves)
-    dec_topk(logits + static_cast<size_t>(t) * E, E, k, s.slot_e + t * k, s.slot_gate + t * k);
+    dec_topk(logits + static_cast<size_t>(t) * E, E, k, w.slot_e + t * k, w.slot_gate + t * k);
   __syncthreads();
-  for (int f = tid; f < T * k; f += kDecThreads) {
-    const int e = s.slot_e[f];
-    // two 16-bit masks per word
-    atomicOr(reinterpret_cast<unsigned int*>(s.mask) + e / 2,
-             (1u << (f / k)) << (16 * (e & 1)));
-  }
+  for (int f = tid; f < T * k; f += kDecThreads) atomicOr(&w.mask[w.slot_e[f]], 1u << (f / k));
   __syncthreads();
   if (wave == 0) {  // compact the used experts; rows in expert order
     int n = 0, rows = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
-      const uint32_t m = e < E ? s.mask[e] : 0u;
+      const uint32_t m = e < E ? w.mask[e] : 0u;
       const uint64_t used = __ballot(m != 0);
       const int before = __popcll(used & ((1ull << lane) - 1));
       const int cnt = __popc(m);
@@ -221,7 +220,7 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
   // the row of each slot: its expert's position by binary search
   const int n = s.n;
   for (int f = tid; f < T * k; f += kDecThreads) {
-    const int e = s.slot_e[f], t = f / k;
+    const int e = w.slot_e[f], t = f / k;
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -230,9 +229,9 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
       else
         hi = mid;
     }
-    const int r = s.base[lo] + __popc(s.mask[e] & ((1u << t) - 1));
+    const int r = s.base[lo] + __popc(w.mask[e] & ((1u << t) - 1));
     s.token[r] = static_cast<uint8_t>(t);
-    s.gate[r] = s.slot_gate[f];
+    s.gate[r] = w.slot_gate[f];
   }
   __syncthreads();
 }
@@ -253,7 +252,8 @@ struct DecLayer {
   static constexpr int kBatch = sizeof(WT) == 1 ? 2 : 4;
   const DecodeArgs& a;
   DecSel& sel;
-  float (*red)[kTok][16];  // [2 * kDecWaves]: sums of 16 rows per token and wave
+  static constexpr int kPasses = kMany ? 4 : 8;  // of W13 between two barriers
+  float (*red)[kTok][16];  // [kPasses * kDecWaves]: sums of 16 rows per token and wave
   uint8_t* lds;            // this wave's weights (kMany)
 
   int lane, wave;
@@ -341,12 +341,15 @@ struct DecLayer {
     const int S = pick_split(g1 - g0);
     const int at_once = kDecWaves / S;
     const int sub = wave % S, gsel = wave / S;
-    int buf = 0;
-    for (int g = g0; g < g1; g += at_once, buf ^= kDecWaves) {
-      if (g + gsel < g1) w13_group((g + gsel) / per, 8 * ((g + gsel) % per), sub, S, buf + wave);
+    for (int g = g0; g < g1; g += kPasses * at_once) {
+      for (int p = 0; p < kPasses; ++p) {
+        const int mine = g + p * at_once + gsel;
+        if (mine < g1) w13_group(mine / per, 8 * (mine % per), sub, S, p * kDecWaves + wave);
+      }
       __syncthreads();
-      // channel pair cp of token column j of group gs
-      for (int o = threadIdx.x; o < at_once * kTok * 4; o += kDecThreads) {
+      // channel pair cp of token column j of the gs-th of these groups, whose
+      // sums are in the S slots from gs * S on
+      for (int o = threadIdx.x; o < kPasses * at_once * kTok * 4; o += kDecThreads) {
         const int cp = o & 3, j = (o >> 2) % kTok, gs = (o >> 2) / kTok;
         if (g + gs >= g1) continue;
         const int i = (g + gs) / per, c = 8 * ((g + gs) % per) + 2 * cp;
@@ -357,8 +360,8 @@ struct DecLayer {
         for (int v = 0; v < 2; ++v) {
           float zg = 0.f, zu = 0.f;
           for (int s = 0; s < S; ++s) {
-            zg += red[buf + gs * S + s][j][2 * cp + v];
-            zu += red[buf + gs * S + s][j][8 + 2 * cp + v];
+            zg += red[gs * S + s][j][2 * cp + v];
+            zu += red[gs * S + s][j][8 + 2 * cp + v];
           }
           if (sizeof(WT) == 1) {
             const size_t e = sel.expert[i];
@@ -381,6 +384,7 @@ struct DecLayer {
           __hip_atomic_store(h + 1, hv[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
       }
+      __syncthreads();  // the sums have been read
     }
   }
 
@@ -560,13 +564,17 @@ template <typename WT, bool kMany>
 __global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs a, int phases) {
   using Layer = DecLayer<WT, kMany>;
   __shared__ DecSel sel;
-  __shared__ __attribute__((aligned(16))) float red[2 * kDecWaves][Layer::kTok][16];
+  // the waves' sums; before them, the selection's scratch
+  __shared__ __attribute__((aligned(16))) union {
+    float red[Layer::kPasses * kDecWaves][Layer::kTok][16];
+    DecScratch scratch;
+  } lds;
   __shared__ __attribute__((aligned(1024))) uint8_t weights[kMany ? kDecWaves : 1]
                                                            [kMany ? 4096 : 16];
   __shared__ int next;
-  dec_select(a.logits, a.T, a.E, a.k, sel);
+  dec_select(a.logits, a.T, a.E, a.k, sel, lds.scratch);
   const int wave = static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
-  const Layer layer{a, sel, red, weights[kMany ? wave : 0], static_cast<int>(threadIdx.x & 63), wave};
+  const Layer layer{a, sel, lds.red, weights[kMany ? wave : 0], static_cast<int>(threadIdx.x & 63), wave};
   if (phases & 1) {
     int64_t limit = a.wait_limit;
     for (int b = blockIdx.x; b >= 0;) {  // b is wave-uniform
@@ -577,7 +585,11 @@ __global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs
       b = dec_wait(a, limit, &next);
       limit = 0;
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");  // h as the others wrote it
+    // h as the others wrote it: one wave discards what this compute unit and
+    // its XCD hold, the barrier extends that to the other waves (a fence in
+    // every wave, 4096 in all, cost 25 us, this one 3)
+    if (threadIdx.x < 64) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    __syncthreads();
   }
   layer.w2_share(blockIdx.x);
 }

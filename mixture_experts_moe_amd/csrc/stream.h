@@ -384,6 +384,21 @@ struct Stream16 {
   }
 };
 
+// The largest value of a wave, in every lane.
+__device__ __forceinline__ uint32_t stream_wave_max(uint32_t v) {
+#define STREAM_MAX(ctrl) \
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), ctrl, 0xf, 0xf, false)))
+  STREAM_MAX(0x121);  // row_ror:1, 2, 4, 8
+  STREAM_MAX(0x122);
+  STREAM_MAX(0x124);
+  STREAM_MAX(0x128);
+#undef STREAM_MAX
+  auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(static_cast<uint32_t>(a[0]), static_cast<uint32_t>(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(static_cast<uint32_t>(b[0]), static_cast<uint32_t>(b[1]));
+}
+
 // Sum over the 16 blocks of a wave, four rows of 16 lanes first: afterwards
 // lane l holds its row of 16 lanes' sum for token l % 4.
 __device__ __forceinline__ float stream_row_sum(float v) {
@@ -395,9 +410,12 @@ __device__ __forceinline__ float stream_row_sum(float v) {
 }
 __device__ __forceinline__ float stream_wave_sum(float v) {
   v = stream_row_sum(v);
-  v += __shfl_xor(v, 16, kWave);
-  v += __shfl_xor(v, 32, kWave);
-  return v;
+  // rows of 16 lanes 0 <-> 1, 2 <-> 3, then the halves: each swap leaves both
+  // sides' values in the pair of results
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 }  // namespace moe
