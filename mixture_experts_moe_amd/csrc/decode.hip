@@ -249,12 +249,13 @@ struct DecLayer {
   using S16 = Stream16<WT, 1, true, kHalf>;
   static constexpr int kTok = kMany ? 16 : 4;  // token columns of an expert
   // chunks of 16 rows in flight per wave (e4m3fn tokens take twice the registers)
-  static constexpr int kBatch = sizeof(WT) == 1 ? 2 : 4;
+  static constexpr int kBatch = (sizeof(WT) == 1 ? 2 : 4) * (kMany ? 2 : 1);
   const DecodeArgs& a;
   DecSel& sel;
   static constexpr int kPasses = kMany ? 4 : 8;  // of W13 between two barriers
   float (*red)[kTok][16];  // [kPasses * kDecWaves]: sums of 16 rows per token and wave
-  uint8_t* lds;            // this wave's weights (kMany)
+  uint8_t* lds0;           // this wave's weights (kMany)
+  uint8_t* lds1;
 
   int lane, wave;
 
@@ -285,7 +286,8 @@ struct DecLayer {
       st.wq[0][1] = up;
       auto row_off = [&](int, int r) { return static_cast<uint32_t>((r & 7) * ldb); };
       st.place(0, [&](int r) { return row_off(0, r); });
-      st.lds = lds;
+      st.lds[0] = lds0;
+      st.lds[1] = lds1;
       token(static_cast<const AT*>(a.x), a.d, base, n, lane & 15, false, &st.xb, &st.xo);
       st.xo += (lane >> 4) * (G::kLaneK * sizeof(AT));
       f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -417,7 +419,8 @@ struct DecLayer {
       st.wq[0][1] = w + 8 * ldb;
       auto row_off = [&](int, int r) { return static_cast<uint32_t>((r & 7) * ldb); };
       st.place(0, [&](int r) { return row_off(0, r); });
-      st.lds = lds;
+      st.lds[0] = lds0;
+      st.lds[1] = lds1;
       token(static_cast<const AT*>(a.h), a.I, base, n, lane & 15, true, &st.xb, &st.xo);
       st.xo += (lane >> 4) * (G::kLaneK * sizeof(AT));
       f32x4 acc[1] = {f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -437,7 +440,7 @@ struct DecLayer {
     f32x4 acc[RQ][1];
 #pragma unroll
     for (int q = 0; q < RQ; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    st.template run<RQ == 2 ? 2 * kBatch : kBatch>(c0, min(c1, full) - c0, 1, acc);
+    st.template run<RQ == 2 && !kMany ? 2 * kBatch : kBatch>(c0, min(c1, full) - c0, 1, acc);
     if (c1 > full) st.tail(full, left, acc);
 #pragma unroll
     for (int q = 0; q < RQ; ++q) {
@@ -561,7 +564,7 @@ __device__ __forceinline__ int dec_wait(const DecodeArgs& a, int64_t limit, int*
 }
 
 template <typename WT, bool kMany>
-__global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs a, int phases) {
+__global__ __launch_bounds__(kDecThreads, kMany ? 2 : 4) void decode_layer_kernel(DecodeArgs a, int phases) {
   using Layer = DecLayer<WT, kMany>;
   __shared__ DecSel sel;
   // the waves' sums; before them, the selection's scratch
@@ -569,12 +572,13 @@ __global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs
     float red[Layer::kPasses * kDecWaves][Layer::kTok][16];
     DecScratch scratch;
   } lds;
-  __shared__ __attribute__((aligned(1024))) uint8_t weights[kMany ? kDecWaves : 1]
-                                                           [kMany ? 4096 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kMany ? kDecWaves : 1][kMany ? 4096 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t w1[kMany ? kDecWaves : 1][kMany ? 4096 : 16];
   __shared__ int next;
   dec_select(a.logits, a.T, a.E, a.k, sel, lds.scratch);
   const int wave = static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
-  const Layer layer{a, sel, lds.red, weights[kMany ? wave : 0], static_cast<int>(threadIdx.x & 63), wave};
+  const Layer layer{a, sel, lds.red, w0[kMany ? wave : 0], w1[kMany ? wave : 0],
+                    static_cast<int>(threadIdx.x & 63), wave};
   if (phases & 1) {
     int64_t limit = a.wait_limit;
     for (int b = blockIdx.x; b >= 0;) {  // b is wave-uniform
@@ -596,8 +600,12 @@ __global__ __launch_bounds__(kDecThreads, 4) void decode_layer_kernel(DecodeArgs
 
 // ------------------------------------------------------------ launchers
 
-// As many workgroups as are resident at once: two of eight waves per unit.
-int decode_workgroups(int cus) { return 2 * cus < kDecMaxWgs ? 2 * cus : kDecMaxWgs; }
+// As many workgroups as are resident at once: with at most four tokens two of
+// eight waves per unit, else one (more registers and LDS per wave).
+int decode_workgroups(int T, int cus) {
+  const int n = T <= 4 ? 2 * cus : cus;
+  return n < kDecMaxWgs ? n : kDecMaxWgs;
+}
 
 size_t decode_flag_bytes() { return kDecFlagBytes; }
 

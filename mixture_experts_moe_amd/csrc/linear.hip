@@ -984,7 +984,7 @@ constexpr int kLinStreamWaves = kLinStreamThreads / 64;
 // kQuads: at most four tokens, 4x4 MFMAs, else 16x16 (RT tiles of 16 rows;
 // gated: eight gate rows, then eight up rows).
 template <typename WT, int RT, bool kQuads, bool kGated, bool kAligned>
-__global__ __launch_bounds__(kLinStreamThreads, 4) void linear_stream_kernel(LinearArgs a) {
+__global__ __launch_bounds__(kLinStreamThreads, RT > 1 ? 2 : 4) void linear_stream_kernel(LinearArgs a) {
   using G = StreamGeom<WT>;
   using AT = typename G::AT;
   using S16 = Stream16<WT, RT, kAligned>;
@@ -993,9 +993,11 @@ __global__ __launch_bounds__(kLinStreamThreads, 4) void linear_stream_kernel(Lin
   // partial sums of four rows of a token; before them, the waves' weights
   union Lds {
     f32x4 red[kParts][kRows / 4][kTok];
-    uint8_t w[!kQuads && kAligned ? kLinStreamWaves : 1][S16::kLds];
+    uint8_t w[!kQuads && kAligned ? kLinStreamWaves : 1][!kQuads && kAligned ? S16::kLds : 16];
   };
   __shared__ __attribute__((aligned(1024))) Lds lds;
+  __shared__ __attribute__((aligned(1024))) uint8_t w1[!kQuads && kAligned ? kLinStreamWaves : 1]
+                                                      [!kQuads && kAligned ? S16::kLds : 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * kCh;
@@ -1049,7 +1051,8 @@ __global__ __launch_bounds__(kLinStreamThreads, 4) void linear_stream_kernel(Lin
       st.wq[t][1] = first(kGated ? 8 * t : 16 * t + 8, kGated);
       st.place(t, [&](int r) { return row_off(t, r); });
     }
-    st.lds = lds.w[!kQuads && kAligned ? wave : 0];
+    st.lds[0] = lds.w[!kQuads && kAligned ? wave : 0];
+    st.lds[1] = w1[!kQuads && kAligned ? wave : 0];
     st.xb = static_cast<const uint8_t*>(a.x);
     st.xo = static_cast<uint32_t>(min(lane & 15, M - 1) * a.ldx * sizeof(AT)) +
             (lane >> 4) * (G::kLaneK * sizeof(AT));
@@ -1097,14 +1100,10 @@ static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
 template <typename WT, bool kGated>
 static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
   if (a.M <= 4) return launch_stream<WT, 1, true, kGated>(a, s);
-  // Tiles of weight rows that share each token load.  e4m3fn weights are half
-  // the bytes of their tokens, so more tiles pay as long as the grid still
-  // fills the chip: 16 x 14336 x 8192 44 us with one tile, 35 with two, 32
-  // with four; 16 x 4096 x 7168 11.3 and 13.3 us with one and two.
-  const int rt = sizeof(WT) > 1 || a.R < 6144 ? 1 : a.R < 12288 ? 2 : 4;
+  // e4m3fn weights are half the bytes of their tokens, so two tiles sharing
+  // each token load pay as long as the grid still fills the chip.
   if constexpr (sizeof(WT) == 1) {
-    if (rt == 4) return launch_stream<WT, 4, false, kGated>(a, s);
-    if (rt == 2) return launch_stream<WT, 2, false, kGated>(a, s);
+    if (a.R >= 6144) return launch_stream<WT, 2, false, kGated>(a, s);
   }
   return launch_stream<WT, 1, false, kGated>(a, s);
 }

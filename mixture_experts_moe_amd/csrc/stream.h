@@ -230,8 +230,9 @@ struct Stream {
 // every tile of weight rows, where the 4x4 MFMAs need one per four tokens.
 // Their operand (lane l: row l % 16, K unit l / 16) would make a load cover 16
 // rows x 64 bytes, half lines, so aligned rows go through LDS: direct-to-LDS
-// loads of four rows x 256 bytes into the wave's own region, unit u of row r
-// in slot u ^ (r & 15) (the 16 rows read for one unit fall in 16 bank
+// loads of four rows x 256 bytes into the wave's own two regions (in arrays of
+// their own: reads of one then wait for no load into the other), unit u of row
+// r in slot u ^ (r & 15) (the 16 rows read for one unit fall in 16 bank
 // groups).  acc[t]: D column (token) l % 16, rows 4 (l / 16) .. +3 of tile t,
 // already summed over K.
 // kHalf: the tiles have eight rows (the other eight sums mean nothing).
@@ -246,7 +247,7 @@ struct Stream16 {
   uint32_t wo[RT][kAligned ? 4 : 1];
   const uint8_t* xb;      // wave-uniform
   uint32_t xo;            // this lane's token row and K unit, bytes
-  uint8_t* lds;           // the wave's kLds bytes (aligned)
+  uint8_t* lds[2];        // the wave's two regions of kLds bytes (aligned)
 
   static constexpr int kLds = RT * 4096;              // one chunk
   static constexpr int kWStep = 256;
@@ -310,52 +311,83 @@ struct Stream16 {
     }
   }
 
-  __device__ __forceinline__ void chunk(int c, f32x4 (&acc)[RT]) const {
-    Toks x;
-    if constexpr (kAligned) {
+  // Chunk c into region `slot` and its tokens into registers; kLoadCount
+  // vector-memory instructions.
+  static constexpr int kLoadCount = RT * (kHalf ? 2 : 4) + kUnits * G::kTokLoads;
+  __device__ __forceinline__ void fetch(int slot, Toks& x, int c) const {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int i = 0; i < (kHalf ? 2 : 4); ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc(wq[t][i / 2]),
+            (__attribute__((address_space(3))) void*)(lds[slot] + 4096 * t + 1024 * i), 16, wo[t][i],
+            c * kWStep, 0, 2);
+    load_x(x, c);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // kLater: loads issued after the chunk's
+  template <int kLater>
+  __device__ __forceinline__ void use(int slot, const Toks& x, f32x4 (&acc)[RT]) const {
+    // the chunk's loads have landed; the compiler does not see that the LDS
+    // reads below depend on them
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLater) : "memory");
+    const int r16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int i = 0; i < (kHalf ? 2 : 4); ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rsrc(wq[t][i / 2]), (__attribute__((address_space(3))) void*)(lds + 4096 * t + 1024 * i), 16,
-              wo[t][i], c * kWStep, 0, 2);
-      load_x(x, c);
-      // the loads have landed; the compiler does not see that the LDS reads
-      // below depend on them
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      const int r16 = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          acc[t] = mma(*reinterpret_cast<const u32x4*>(lds + 4096 * t + 256 * r16 +
-                                                       16 * ((4 * u + g) ^ r16)),
-                       x[u], acc[t]);
-      // every read has returned before the next chunk's loads overwrite them
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    } else {
-      u32x4 w[kUnits][RT];
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          w[u][t] = reinterpret_cast<const StreamUnit*>(
-                        lane_row(t) + static_cast<size_t>(c) * kWStep + wo[t][0] + 64 * u)
-                        ->v;
-      load_x(x, c);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = mma(w[u][t], x[u], acc[t]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+        acc[t] = mma(*reinterpret_cast<const u32x4*>(lds[slot] + 4096 * t + 256 * r16 +
+                                                     16 * ((4 * u + g) ^ r16)),
+                     x[u], acc[t]);
+    // every read has returned before later loads overwrite the region
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
-  // acc += over chunks c0, c0 + step, ... (n of them), one at a time per wave.
+  __device__ __forceinline__ void direct(int c, f32x4 (&acc)[RT]) const {
+    Toks x;
+    u32x4 w[kUnits][RT];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        w[u][t] = reinterpret_cast<const StreamUnit*>(
+                      lane_row(t) + static_cast<size_t>(c) * kWStep + wo[t][0] + 64 * u)
+                      ->v;
+    load_x(x, c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[t] = mma(w[u][t], x[u], acc[t]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // acc += over chunks c0, c0 + step, ... (n of them), the next one loading
+  // while one is multiplied.
   __device__ __forceinline__ void run(int c0, int n, int step, f32x4 (&acc)[RT]) const {
-    for (; n >= 1; --n, c0 += step) chunk(c0, acc);
+    if constexpr (kAligned) {
+      static_assert(kLoadCount <= 63, "six-bit count");
+      if (n <= 0) return;
+      Toks x0, x1;
+      fetch(0, x0, c0);
+      for (;; n -= 2, c0 += 2 * step) {
+        if (n == 1) {
+          use<0>(0, x0, acc);
+          return;
+        }
+        fetch(1, x1, c0 + step);
+        use<kLoadCount>(0, x0, acc);
+        if (n == 2) {
+          use<0>(1, x1, acc);
+          return;
+        }
+        fetch(0, x0, c0 + 2 * step);
+        use<kLoadCount>(1, x1, acc);
+      }
+    } else {
+      for (; n >= 1; --n, c0 += step) direct(c0, acc);
+    }
   }
 
   // The last, partial chunk: `left` (< kChunk) elements of K; row_off as for
