@@ -248,8 +248,8 @@ struct DecLayer {
   template <bool kHalf>
   using S16 = Stream16<WT, 1, true, kHalf>;
   static constexpr int kTok = kMany ? 16 : 4;  // token columns of an expert
-  // chunks of 16 rows in flight per wave (e4m3fn tokens take twice the registers)
-  static constexpr int kBatch = (sizeof(WT) == 1 ? 2 : 4) * (kMany ? 2 : 1);
+  // chunks of 16 rows in flight per wave
+  static constexpr int kBatch = sizeof(WT) > 1 ? 8 : kMany ? 4 : 2;
   const DecodeArgs& a;
   DecSel& sel;
   static constexpr int kPasses = kMany ? 4 : 8;  // of W13 between two barriers
@@ -440,7 +440,7 @@ struct DecLayer {
     f32x4 acc[RQ][1];
 #pragma unroll
     for (int q = 0; q < RQ; ++q) acc[q][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    st.template run<RQ == 2 && !kMany ? 2 * kBatch : kBatch>(c0, min(c1, full) - c0, 1, acc);
+    st.template run<kBatch>(c0, min(c1, full) - c0, 1, acc);
     if (c1 > full) st.tail(full, left, acc);
 #pragma unroll
     for (int q = 0; q < RQ; ++q) {
@@ -564,7 +564,8 @@ __device__ __forceinline__ int dec_wait(const DecodeArgs& a, int64_t limit, int*
 }
 
 template <typename WT, bool kMany>
-__global__ __launch_bounds__(kDecThreads, kMany ? 2 : 4) void decode_layer_kernel(DecodeArgs a, int phases) {
+__global__ __launch_bounds__(kDecThreads, sizeof(WT) > 1 || kMany ? 2 : 4) void
+decode_layer_kernel(DecodeArgs a, int phases) {
   using Layer = DecLayer<WT, kMany>;
   __shared__ DecSel sel;
   // the waves' sums; before them, the selection's scratch
@@ -600,10 +601,14 @@ __global__ __launch_bounds__(kDecThreads, kMany ? 2 : 4) void decode_layer_kerne
 
 // ------------------------------------------------------------ launchers
 
-// As many workgroups as are resident at once: with at most four tokens two of
-// eight waves per unit, else one (more registers and LDS per wave).
-int decode_workgroups(int T, int cus) {
-  const int n = T <= 4 ? 2 * cus : cus;
+// As many workgroups as are resident at once.  One of eight waves per unit,
+// whose 256 registers hold eight chunks each (two workgroups per unit with
+// four chunks each took 89 us for 4 tokens of d = 2048, E = 64, top-8, I = 1024
+// in bf16 against 78); with e4m3fn weights, which the waves widen as they go,
+// and few tokens two with two chunks each (4 tokens of d = 7168, E = 256,
+// top-8, I = 2048: 248 us against 262).
+int decode_workgroups(int T, int w_dtype, int cus) {
+  const int n = w_dtype == kDtypeE4M3FN && T <= 4 ? 2 * cus : cus;
   return n < kDecMaxWgs ? n : kDecMaxWgs;
 }
 
