@@ -944,7 +944,7 @@ MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate,
   a.E = static_cast<int>(desc->num_experts);
   a.I = static_cast<int>(desc->intermediate);
   a.k = top_k;
-  a.wgs = moe::decode_workgroups(a.T, a.w_dtype, cus);
+  a.wgs = moe::decode_workgroups(cus);
   a.wait_limit = desc->schedule == MOE_SCHED_QUEUE ? 0 : kDecodeWaitTicks;
   hipError_t e =
       timed(MOE_KERNEL_ROUTE_LOGITS, s, [&] { return moe::launch_decode_route(a, s); });

@@ -24,8 +24,13 @@
 
 namespace moe {
 
-constexpr int kDecThreads = 512;
-constexpr int kDecWaves = kDecThreads / 64;
+// Waves of a workgroup, one workgroup per compute unit: eight, whose 256
+// registers hold eight chunks in flight each (two such workgroups per unit
+// with four chunks each took 89 us for 4 tokens of d = 2048, E = 64, top-8,
+// I = 1024 in bf16 against 78); sixteen with e4m3fn weights, which the waves
+// widen as they go, and few tokens.
+template <typename WT, bool kMany>
+constexpr int dec_waves() { return sizeof(WT) == 1 && !kMany ? 16 : 8; }
 constexpr int kDecMaxRows = kDecodeMaxTokens * kMaxTopK;  // slots
 constexpr int kDecMaxWgs = 1024;
 constexpr int kDecGroup = 32;                        // workgroups of a group
@@ -114,6 +119,7 @@ struct DecScratch {
   float slot_gate[kDecMaxRows];
   uint32_t mask[kMaxExperts];  // bit t: token t selected this expert
   uint16_t slot_e[kDecMaxRows];
+  uint16_t first[kMaxExperts];  // an expert's first row
 };
 
 // Order-preserving key: greater logit, greater key; NaN as -inf; both zeros
@@ -131,9 +137,9 @@ __device__ __forceinline__ float dec_logit(uint32_t key) {
 // One wave selects the top k of a token's E logits: lane l holds experts
 // l*per .. l*per+per-1, so the first lane holding the maximum has the lowest
 // index; gates = softmax over the selection.
+template <int kPer>  // E <= 64 * kPer
 __device__ __forceinline__ void dec_topk(const float* row, int E, int k, uint16_t* slot_e,
                                          float* slot_gate) {
-  constexpr int kPer = kMaxExperts / 64;
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
   uint32_t key[kPer];
@@ -180,15 +186,22 @@ __device__ __forceinline__ void dec_topk(const float* row, int E, int k, uint16_
   }
 }
 
+template <int kWaves>
 __device__ __forceinline__ void dec_select(const float* logits, int T, int E, int k, DecSel& s,
                                            DecScratch& w) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < E; e += kDecThreads) w.mask[e] = 0;
-  for (int t = wave; t < T; t += kDecWaves)
-    dec_topk(logits + static_cast<size_t>(t) * E, E, k, w.slot_e + t * k, w.slot_gate + t * k);
+  constexpr int kThreads = 64 * kWaves;
+  for (int e = tid; e < E; e += kThreads) w.mask[e] = 0;
+  for (int t = wave; t < T; t += kWaves) {
+    const float* row = logits + static_cast<size_t>(t) * E;
+    if (E <= 256)
+      dec_topk<4>(row, E, k, w.slot_e + t * k, w.slot_gate + t * k);
+    else
+      dec_topk<kMaxExperts / 64>(row, E, k, w.slot_e + t * k, w.slot_gate + t * k);
+  }
   __syncthreads();
-  for (int f = tid; f < T * k; f += kDecThreads) atomicOr(&w.mask[w.slot_e[f]], 1u << (f / k));
+  for (int f = tid; f < T * k; f += kThreads) atomicOr(&w.mask[w.slot_e[f]], 1u << (f / k));
   __syncthreads();
   if (wave == 0) {  // compact the used experts; rows in expert order
     int n = 0, rows = 0;
@@ -198,18 +211,22 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
       const uint64_t used = __ballot(m != 0);
       const int before = __popcll(used & ((1ull << lane) - 1));
       const int cnt = __popc(m);
-      int incl = cnt;  // rows up to and with this lane's expert
+      // rows before this lane's expert (cnt <= 16: five bits)
+      const uint64_t below = (1ull << lane) - 1;
+      int first = rows, all = 0;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(incl, off, 64);
-        if (lane >= off) incl += o;
+      for (int bit = 0; bit < 5; ++bit) {
+        const uint64_t set = __ballot((cnt >> bit) & 1);
+        first += __popcll(set & below) << bit;
+        all += __popcll(set) << bit;
       }
       if (m) {
         s.expert[n + before] = static_cast<uint16_t>(e);
-        s.base[n + before] = static_cast<uint16_t>(rows + incl - cnt);
+        s.base[n + before] = static_cast<uint16_t>(first);
+        w.first[e] = static_cast<uint16_t>(first);
       }
       n += __popcll(used);
-      rows += __shfl(incl, 63, 64);
+      rows += all;
     }
     if (lane == 0) {
       s.base[n] = static_cast<uint16_t>(rows);
@@ -217,19 +234,9 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
     }
   }
   __syncthreads();
-  // the row of each slot: its expert's position by binary search
-  const int n = s.n;
-  for (int f = tid; f < T * k; f += kDecThreads) {
+  for (int f = tid; f < T * k; f += kThreads) {
     const int e = w.slot_e[f], t = f / k;
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s.expert[mid] < e)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    const int r = s.base[lo] + __popc(w.mask[e] & ((1u << t) - 1));
+    const int r = w.first[e] + __popc(w.mask[e] & ((1u << t) - 1));
     s.token[r] = static_cast<uint8_t>(t);
     s.gate[r] = w.slot_gate[f];
   }
@@ -248,16 +255,28 @@ struct DecLayer {
   template <bool kHalf>
   using S16 = Stream16<WT, 1, true, kHalf>;
   static constexpr int kTok = kMany ? 16 : 4;  // token columns of an expert
+  static constexpr int kWaves = dec_waves<WT, kMany>(), kThreads = 64 * kWaves;
   // chunks of 16 rows in flight per wave
   static constexpr int kBatch = sizeof(WT) > 1 ? 8 : kMany ? 4 : 2;
   const DecodeArgs& a;
   DecSel& sel;
-  static constexpr int kPasses = kMany ? 4 : 8;  // of W13 between two barriers
-  float (*red)[kTok][16];  // [kPasses * kDecWaves]: sums of 16 rows per token and wave
+  // Work inside the workgroup goes in units that the waves take from a counter
+  // in LDS (the memory serves older waves first: with equal shares some
+  // finished in two thirds of the others' time).  A unit's sums have a slot of
+  // their own, so they are the same whichever wave takes it.
+  static constexpr int kSlots = kMany ? 32 : 8 * kWaves;
+  float (*red)[kTok][16];  // [kSlots]: a unit's sums of 16 rows per token
+  int* ticket;
   uint8_t* lds0;           // this wave's weights (kMany)
   uint8_t* lds1;
 
   int lane, wave;
+
+  __device__ __forceinline__ int take() const {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(ticket, 1);
+    return uniform(u);
+  }
 
   // The lane's token row (of n rows from `base`; columns past the last repeat
   // it, never stored): wave-uniform base and byte offset.
@@ -323,8 +342,8 @@ struct DecLayer {
   __device__ __forceinline__ int pick_split(int groups) const {
     const int chunks = (a.d + G::kChunk - 1) / G::kChunk;
     int best = 1 << 30, s = 1;
-    for (int S = 1; S <= kDecWaves; S *= 2) {
-      const int passes = (groups * S + kDecWaves - 1) / kDecWaves;
+    for (int S = 1; S <= 8; S *= 2) {
+      const int passes = (groups * S + kWaves - 1) / kWaves;
       const int cost = passes * ((chunks + S - 1) / S + 2);
       if (cost < best) {
         best = cost;
@@ -341,19 +360,18 @@ struct DecLayer {
     const int g0 = static_cast<int>(total * b / a.wgs);
     const int g1 = static_cast<int>(total * (b + 1) / a.wgs);
     const int S = pick_split(g1 - g0);
-    const int at_once = kDecWaves / S;
-    const int sub = wave % S, gsel = wave / S;
-    for (int g = g0; g < g1; g += kPasses * at_once) {
-      for (int p = 0; p < kPasses; ++p) {
-        const int mine = g + p * at_once + gsel;
-        if (mine < g1) w13_group(mine / per, 8 * (mine % per), sub, S, p * kDecWaves + wave);
-      }
+    const int rounds = ((g1 - g0) * S + kSlots - 1) / kSlots;
+    const int step = rounds ? (g1 - g0 + rounds - 1) / rounds : 1;  // groups of a round
+    for (int g = g0; g < g1; g += step) {
+      const int n = min(step, g1 - g);
+      for (int u = take(); u < n * S; u = take())
+        w13_group((g + u / S) / per, 8 * ((g + u / S) % per), u % S, S, u);
       __syncthreads();
+      if (threadIdx.x == 0) *ticket = 0;
       // channel pair cp of token column j of the gs-th of these groups, whose
       // sums are in the S slots from gs * S on
-      for (int o = threadIdx.x; o < kPasses * at_once * kTok * 4; o += kDecThreads) {
+      for (int o = threadIdx.x; o < n * kTok * 4; o += kThreads) {
         const int cp = o & 3, j = (o >> 2) % kTok, gs = (o >> 2) / kTok;
-        if (g + gs >= g1) continue;
         const int i = (g + gs) / per, c = 8 * ((g + gs) % per) + 2 * cp;
         const int base = sel.base[i];
         if (j >= sel.base[i + 1] - base) continue;
@@ -392,10 +410,11 @@ struct DecLayer {
 
   // ---- W2: output rows r0 .. r0+4*RQ-1.
 
-  // four rows' sums v of one expert for token column j, into the wave's out sums
-  __device__ __forceinline__ void add(int e, int base, int j, int r0, int r, f32x4 v) const {
+  // four rows' sums v of one expert for token column j, into the unit's out sums
+  __device__ __forceinline__ void add(int slot, int e, int base, int j, int r0, int r,
+                                      f32x4 v) const {
     const float gate = sel.gate[base + j];
-    float* o = &red[wave][sel.token[base + j]][r];
+    float* o = &red[slot][sel.token[base + j]][r];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (sizeof(WT) == 1)
@@ -405,19 +424,22 @@ struct DecLayer {
   }
 
   // chunks [c0, c1) of selected expert i (the last may be partial); adds the
-  // expert's gated, scaled sums to the wave's out sums
+  // expert's gated, scaled sums to the unit's out sums
   template <int RQ>
-  __device__ __forceinline__ void w2_part(int i, int r0, int c0, int c1) const {
+  __device__ __forceinline__ void w2_part(int slot, int i, int r0, int c0, int c1) const {
     const int e = uniform(sel.expert[i]), base = uniform(sel.base[i]);
     const int n = uniform(sel.base[i + 1]) - base;
     const size_t ldb = static_cast<size_t>(a.I) * sizeof(WT);
     const uint8_t* w = static_cast<const uint8_t*>(a.w2) + (static_cast<size_t>(e) * a.d + r0) * ldb;
     const int full = a.I / G::kChunk, left = a.I % G::kChunk;
     if (kMany && n > 4) {
-      S16<RQ == 2> st;
+      S16<(RQ <= 2)> st;
       st.wq[0][0] = w;
       st.wq[0][1] = w + 8 * ldb;
-      auto row_off = [&](int, int r) { return static_cast<uint32_t>((r & 7) * ldb); };
+      // rows past the last repeat it
+      auto row_off = [&](int, int r) {
+        return static_cast<uint32_t>((min(r, 4 * RQ - 1) - (r & 8)) * ldb);
+      };
       st.place(0, [&](int r) { return row_off(0, r); });
       st.lds[0] = lds0;
       st.lds[1] = lds1;
@@ -427,7 +449,7 @@ struct DecLayer {
       st.run(c0, min(c1, full) - c0, 1, acc);
       if (c1 > full) st.tail(full, left, row_off, acc);
       const int j = lane & 15, r = 4 * (lane >> 4);
-      if (j < n && r < 4 * RQ) add(e, base, j, r0, r, acc[0]);
+      if (j < n && r < 4 * RQ) add(slot, e, base, j, r0, r, acc[0]);
       return;
     }
     Stream<WT, RQ, 1, true> st;
@@ -446,33 +468,35 @@ struct DecLayer {
     for (int q = 0; q < RQ; ++q) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[q][0][v] = stream_wave_sum(acc[q][0][v]);
-      if (lane < n) add(e, base, lane, r0, 4 * q, acc[q][0]);
+      if (lane < n) add(slot, e, base, lane, r0, 4 * q, acc[q][0]);
     }
   }
 
   template <int RQ>
   __device__ __forceinline__ void w2_rows(int r0) const {
     const int tid = threadIdx.x;
-    __syncthreads();  // the sums before have been read
-    for (int o = tid; o < kDecWaves * kTok * 16; o += kDecThreads)
-      (&red[0][0][0])[o] = 0.f;
-    __syncthreads();
-    // the waves share the (expert, chunk) list evenly
+    // the (expert, chunk) list in equal units, as many for each wave, of at
+    // least 16 chunks where there are enough
     const int C = (a.I + G::kChunk - 1) / G::kChunk;
     const int items = uniform(sel.n) * C;
-    const int i0 = items * wave / kDecWaves, i1 = items * (wave + 1) / kDecWaves;
-    for (int it = i0; it < i1;) {
-      const int i = it / C, c0 = it % C;
-      const int c1 = min(C, c0 + i1 - it);
-      w2_part<RQ>(i, r0, c0, c1);
-      it += c1 - c0;
+    const int units = kWaves * min(max(items / (16 * kWaves), 1), kMany ? kSlots / kWaves : 4);
+    for (int o = tid; o < units * kTok * 16; o += kThreads) (&red[0][0][0])[o] = 0.f;
+    if (tid == 0) *ticket = 0;
+    __syncthreads();
+    for (int u = take(); u < units; u = take()) {
+      const int i1 = static_cast<int>(static_cast<int64_t>(items) * (u + 1) / units);
+      for (int it = static_cast<int>(static_cast<int64_t>(items) * u / units); it < i1;) {
+        const int i = it / C, c0 = it % C;
+        const int c1 = min(C, c0 + i1 - it);
+        w2_part<RQ>(u, i, r0, c0, c1);
+        it += c1 - c0;
+      }
     }
     __syncthreads();
-    for (int o = tid; o < a.T * 4 * RQ; o += kDecThreads) {
+    for (int o = tid; o < a.T * 4 * RQ; o += kThreads) {
       const int t = o / (4 * RQ), r = o % (4 * RQ);
       float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kDecWaves; ++w) v += red[w][t][r];
+      for (int u = 0; u < units; ++u) v += red[u][t][r];
       const size_t at = static_cast<size_t>(t) * a.d + r0 + r;
       if constexpr (sizeof(AT) == 2) {
         if (a.res) v += bf16_to_f32(static_cast<const bf16_t*>(a.res)[at]);
@@ -482,14 +506,19 @@ struct DecLayer {
         static_cast<float*>(a.out)[at] = v;
       }
     }
+    __syncthreads();  // the sums have been read
   }
 
   __device__ void w2_share(int b) const {
-    const int pairs = a.d / 8;  // of row quads
-    const int p1 = static_cast<int>(static_cast<int64_t>(pairs) * (b + 1) / a.wgs);
-    int p = static_cast<int>(static_cast<int64_t>(pairs) * b / a.wgs);
-    for (; p + 2 <= p1; p += 2) w2_rows<4>(8 * p);
-    if (p < p1) w2_rows<2>(8 * p);
+    const int quads = a.d / 4;
+    const int q1 = static_cast<int>(static_cast<int64_t>(quads) * (b + 1) / a.wgs);
+    int q = static_cast<int>(static_cast<int64_t>(quads) * b / a.wgs);
+    for (; q + 4 <= q1; q += 4) w2_rows<4>(4 * q);
+    switch (q1 - q) {
+      case 3: w2_rows<3>(4 * q); break;
+      case 2: w2_rows<2>(4 * q); break;
+      case 1: w2_rows<1>(4 * q); break;
+    }
   }
 };
 
@@ -564,21 +593,22 @@ __device__ __forceinline__ int dec_wait(const DecodeArgs& a, int64_t limit, int*
 }
 
 template <typename WT, bool kMany>
-__global__ __launch_bounds__(kDecThreads, sizeof(WT) > 1 || kMany ? 2 : 4) void
+__global__ __launch_bounds__((64 * dec_waves<WT, kMany>()), (dec_waves<WT, kMany>() / 4)) void
 decode_layer_kernel(DecodeArgs a, int phases) {
   using Layer = DecLayer<WT, kMany>;
   __shared__ DecSel sel;
-  // the waves' sums; before them, the selection's scratch
+  // the units' sums; before them, the selection's scratch
   __shared__ __attribute__((aligned(16))) union {
-    float red[Layer::kPasses * kDecWaves][Layer::kTok][16];
+    float red[Layer::kSlots][Layer::kTok][16];
     DecScratch scratch;
   } lds;
-  __shared__ __attribute__((aligned(1024))) uint8_t w0[kMany ? kDecWaves : 1][kMany ? 4096 : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t w1[kMany ? kDecWaves : 1][kMany ? 4096 : 16];
-  __shared__ int next;
-  dec_select(a.logits, a.T, a.E, a.k, sel, lds.scratch);
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kMany ? 8 : 1][kMany ? 4096 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t w1[kMany ? 8 : 1][kMany ? 4096 : 16];
+  __shared__ int next, ticket;
+  if (threadIdx.x == 0) ticket = 0;
+  dec_select<Layer::kWaves>(a.logits, a.T, a.E, a.k, sel, lds.scratch);
   const int wave = static_cast<int>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
-  const Layer layer{a, sel, lds.red, w0[kMany ? wave : 0], w1[kMany ? wave : 0],
+  const Layer layer{a, sel, lds.red, &ticket, w0[kMany ? wave : 0], w1[kMany ? wave : 0],
                     static_cast<int>(threadIdx.x & 63), wave};
   if (phases & 1) {
     int64_t limit = a.wait_limit;
@@ -601,16 +631,7 @@ decode_layer_kernel(DecodeArgs a, int phases) {
 
 // ------------------------------------------------------------ launchers
 
-// As many workgroups as are resident at once.  One of eight waves per unit,
-// whose 256 registers hold eight chunks each (two workgroups per unit with
-// four chunks each took 89 us for 4 tokens of d = 2048, E = 64, top-8, I = 1024
-// in bf16 against 78); with e4m3fn weights, which the waves widen as they go,
-// and few tokens two with two chunks each (4 tokens of d = 7168, E = 256,
-// top-8, I = 2048: 248 us against 262).
-int decode_workgroups(int T, int w_dtype, int cus) {
-  const int n = w_dtype == kDtypeE4M3FN && T <= 4 ? 2 * cus : cus;
-  return n < kDecMaxWgs ? n : kDecMaxWgs;
-}
+int decode_workgroups(int cus) { return cus < kDecMaxWgs ? cus : kDecMaxWgs; }
 
 size_t decode_flag_bytes() { return kDecFlagBytes; }
 
@@ -629,9 +650,9 @@ hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s) {
 template <typename WT>
 static hipError_t layer(const DecodeArgs& a, int phases, hipStream_t s) {
   if (a.T <= 4)
-    decode_layer_kernel<WT, false><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
+    decode_layer_kernel<WT, false><<<a.wgs, 64 * dec_waves<WT, false>(), 0, s>>>(a, phases);
   else
-    decode_layer_kernel<WT, true><<<a.wgs, kDecThreads, 0, s>>>(a, phases);
+    decode_layer_kernel<WT, true><<<a.wgs, 64 * dec_waves<WT, true>(), 0, s>>>(a, phases);
   return hipGetLastError();
 }
 

@@ -275,7 +275,7 @@ struct DecodeArgs {
 };
 
 // Workgroups of the layer launch that `cus` compute units hold at once.
-int decode_workgroups(int T, int w_dtype, int cus);
+int decode_workgroups(int cus);
 size_t decode_flag_bytes();
 hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s);
 // phases: 1 = W13, 2 = W2 and the sum over experts, 3 = both in one launch.

@@ -257,7 +257,8 @@ struct Stream16 {
 
   using Toks = u32x4[kUnits][G::kTokLoads];
 
-  // The offsets of tile t: row_off(r) = bytes to row r from its half's base.
+  // The offsets of tile t: row_off(r) = bytes to row r from its half's base
+  // (rows 0 and 8).
   template <class F>
   __device__ __forceinline__ void place(int t, F row_off) {
     const int lane = threadIdx.x & 63;
