@@ -533,6 +533,53 @@ def moe_route_align(x: torch.Tensor, w_gate: torch.Tensor, top_k: int, *, interm
     return logits, ids, w, counts, sorted_ids[:cap], block_expert[:cap // B], num_padded[:1], B
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _one_gpu(*ts: Optional[torch.Tensor]) -> int:
+    """The index of the GPU that holds every tensor given."""
+    index = -1
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on the GPU")
+        i = t.get_device()
+        if index >= 0 and i != index:
+            raise ValueError("all tensors must be on one device")
+        index = i
+    return index
+
+
+def _allocator(dev: torch.device, index: int, stream):
+    """(hipStream_t, allocate(shape, dtype)): tensors belong to the launch
+    stream, which torch's allocator takes without a stream switch where it is
+    the current one."""
+    current = torch.cuda.current_stream(index)
+    if stream is None or stream == current:
+        return current.cuda_stream, lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    return stream.cuda_stream, lambda shape, dtype: _alloc(shape, dtype, dev, stream)
+
+
+class _Here:
+    """No device switch."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(index: int):
+    """The tensors' device made current for the launch, where it is not."""
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
 def moe_decode_workspace_bytes(desc: moe_desc, top_k: int) -> int:
     n = ctypes.c_size_t()
     _check("moe_decode_workspace_bytes",
@@ -554,19 +601,25 @@ def moe_decode(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: tor
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError(f"residual must match x in shape and dtype: residual "
                          f"{tuple(residual.shape)} {residual.dtype}, x {tuple(x.shape)} {x.dtype}")
-    dev = _dev(x, w_gate, w13, w2, residual, out)
+    _dev(x, w_gate, w13, w2, residual, out)
+    index = x.get_device()
     desc = make_desc(T, d, E, I, _act_code(x), _w_code(w13), 0, None, schedule)
+    ref = ctypes.byref(desc)
     sc = _scales(w13, scales)
-    s = _launch_stream(dev, stream)
+    s, new = _allocator(x.device, index, stream)
     if out is None:
-        out = _alloc((T, d), x.dtype, dev, s)
-    nbytes = moe_decode_workspace_bytes(desc, top_k)
-    ws = _workspace(nbytes, dev, workspace, s)
-    st = lib().moe_decode(ctypes.byref(desc), _ptr(x), _ptr(w_gate), _ptr(w13), _ptr(w2),
-                          int(top_k), ctypes.byref(sc) if sc is not None else None,
-                          _ptr(residual), _ptr(out), _ptr(ws), nbytes,
-                          ctypes.c_void_p(s.cuda_stream))
-    _check("moe_decode", st)
+        out = new((T, d), x.dtype)
+    nbytes = ctypes.c_size_t()
+    _check("moe_decode_workspace_bytes",
+           lib().moe_decode_workspace_bytes(ref, int(top_k), nbytes))
+    ws = workspace if workspace is not None else new((max(nbytes.value, 1),), torch.uint8)
+    if ws.numel() * ws.element_size() < nbytes.value:
+        raise ValueError("workspace too small")
+    with _on(index):
+        _check("moe_decode", lib().moe_decode(
+            ref, x.data_ptr(), w_gate.data_ptr(), w13.data_ptr(), w2.data_ptr(), int(top_k),
+            ctypes.byref(sc) if sc is not None else None, _addr(residual), out.data_ptr(),
+            ws.data_ptr(), nbytes.value, s))
     return out
 
 
@@ -575,12 +628,13 @@ _FNS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 def _rows(name: str, t: torch.Tensor, shape) -> int:
     """The row stride of a matrix of the given shape whose rows are dense."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have dense rows, got strides {tuple(t.stride())}")
-    return t.stride(0) if rows > 1 else cols
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have dense rows, got strides {(ld, step)}")
+    return ld if rows > 1 else cols
 
 
 def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
@@ -626,26 +680,27 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
         if out.dtype != x.dtype:
             raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
         ldo = _rows("out", out, (M, N))
-    dev = _dev(scale, bias)     # contiguous; the matrices only need dense rows
-    for t in (x, w, residual, out):
-        if t is not None:
-            if t.device.type != "cuda":
-                raise ValueError("all tensors must be on the GPU")
-            if dev is not None and t.device != dev:
-                raise ValueError("all tensors must be on one device")
-            dev = t.device
+    index = _one_gpu(x, w, scale, bias, residual, out)
+    for t in (scale, bias):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("scale and bias must be contiguous")
     desc = moe_linear_desc(M, N, K, ldx, ldw, ldr, ldo, act, wdt, _FNS[activation],
-                           int(bool(gated)), mode, 0)
-    s = _launch_stream(dev, stream)
+                           1 if gated else 0, mode, 0)
+    ref = ctypes.byref(desc)
+    s, new = _allocator(x.device, index, stream)
     if out is None:
-        out = _alloc((M, N), x.dtype, dev, s)
-    n = ctypes.c_size_t()
-    _check("moe_linear_workspace_bytes",
-           lib().moe_linear_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)))
-    ws = _workspace(n.value, dev, workspace, s) if n.value else None
-    _check("moe_linear", lib().moe_linear(
-        ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(scale), _ptr(bias), _ptr(residual), _ptr(out),
-        _ptr(ws), n.value, ctypes.c_void_p(s.cuda_stream)))
+        out = new((M, N), x.dtype)
+    nbytes = ctypes.c_size_t()
+    _check("moe_linear_workspace_bytes", lib().moe_linear_workspace_bytes(ref, nbytes))
+    ws = None
+    if nbytes.value:
+        ws = workspace if workspace is not None else new((nbytes.value,), torch.uint8)
+        if ws.numel() * ws.element_size() < nbytes.value:
+            raise ValueError("workspace too small")
+    with _on(index):
+        _check("moe_linear", lib().moe_linear(
+            ref, x.data_ptr(), w.data_ptr(), _addr(scale), _addr(bias), _addr(residual),
+            out.data_ptr(), _addr(ws), nbytes.value, s))
     return out
 
 
