@@ -864,7 +864,7 @@ MOE_API int moe_graph_destroy(moe_graph* graph) {
 constexpr int64_t kDecodeWaitTicks = 200000;
 
 struct DecodePlan {
-  size_t logits, flags, h, total;
+  size_t logits, meet, h, total;
 };
 
 static int check_decode(const moe_desc* d, int top_k, DecodePlan* p) {
@@ -875,8 +875,8 @@ static int check_decode(const moe_desc* d, int top_k, DecodePlan* p) {
   if (d->num_tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_BAD_SHAPE;
   const size_t T = static_cast<size_t>(d->num_tokens);
   p->logits = 0;
-  p->flags = round_up(T * d->num_experts * 4, kWsAlign);
-  p->h = p->flags + round_up(moe::decode_flag_bytes(), kWsAlign);
+  p->meet = round_up(T * d->num_experts * 4, kWsAlign);
+  p->h = p->meet + round_up(moe::decode_meet_bytes(), kWsAlign);
   p->total = T ? p->h + round_up(T * top_k * d->intermediate * act_bytes(d->act_dtype), kWsAlign)
                : 0;
   return MOE_OK;
@@ -937,7 +937,7 @@ MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate,
   a.res = residual;
   a.out = out;
   a.logits = reinterpret_cast<float*>(ws + p.logits);
-  a.flags = reinterpret_cast<uint8_t*>(ws + p.flags);
+  a.meet = reinterpret_cast<uint8_t*>(ws + p.meet);
   a.h = ws + p.h;
   a.T = static_cast<int>(desc->num_tokens);
   a.d = static_cast<int>(desc->hidden);

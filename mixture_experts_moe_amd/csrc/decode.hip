@@ -32,17 +32,33 @@ namespace moe {
 template <typename WT, bool kMany>
 constexpr int dec_waves() { return sizeof(WT) == 1 && !kMany ? 16 : 8; }
 constexpr int kDecMaxRows = kDecodeMaxTokens * kMaxTopK;  // slots
-constexpr int kDecMaxWgs = 1024;
-constexpr int kDecGroup = 32;                        // workgroups of a group
+constexpr int kDecMaxWgs = 256;
+constexpr int kDecGroup = 32;  // workgroups that share a go word
 constexpr int kDecGroups = kDecMaxWgs / kDecGroup;
-constexpr int kDecLine = 128;
-// a byte per workgroup, then lines: the groups' counters, their go words, the
-// counter of groups
-constexpr int kDecFlagBytes = kDecMaxWgs + (2 * kDecGroups + 1) * kDecLine;
+// Words that workgroups meet through, each in a cache line of its own (hundreds
+// of workgroups polling, adding to or storing to one line take tens of
+// microseconds): a flag per workgroup, a go word per group, a counter per row
+// quad whose sum is split over workgroups.
+constexpr int kDecLine = 64;
+constexpr int kDecFlag = 0, kDecGo = kDecMaxWgs, kDecCount = kDecGo + kDecGroups;
+constexpr int kDecLines = kDecCount + kDecMaxWgs / 2;
+constexpr int kDecMeetBytes = kDecLines * kDecLine;
+// and the split sums: [workgroup][token][4 rows] fp32
+constexpr int kDecSumBytes = kDecMaxWgs * kDecodeMaxTokens * 4 * 4;
 
 // A value that every lane holds alike, as a scalar: addresses built from it
 // stay in scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int32_t* dec_word(const DecodeArgs& a, int i) {
+  return reinterpret_cast<int32_t*>(a.meet + i * kDecLine);
+}
+__device__ __forceinline__ int dec_read(const int32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void dec_write(int32_t* p, int v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 // ------------------------------------------------------------ router logits
 
@@ -54,14 +70,15 @@ constexpr int kRouteTokens = 4;
 template <typename AT>
 __global__ __launch_bounds__(kRouteThreads) void decode_route_kernel(
     const AT* __restrict__ x, const float* __restrict__ w_gate, float* __restrict__ logits,
-    uint8_t* __restrict__ flags, int T, int E, int d) {
+    uint8_t* __restrict__ meet, int T, int E, int d) {
   __shared__ float part[kRouteThreads / 64][kRouteTokens];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e = blockIdx.x, t0 = blockIdx.y * kRouteTokens;
   const int n = min(T - t0, kRouteTokens);
-  if (e == 0 && t0 == 0)
-    for (int i = tid; i < kDecFlagBytes / 4; i += kRouteThreads)
-      reinterpret_cast<uint32_t*>(flags)[i] = 0;
+  // this launch clears the meeting words of the next, a slice per workgroup
+  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kRouteThreads + tid; i < kDecMeetBytes / 16;
+       i += gridDim.x * gridDim.y * kRouteThreads)
+    reinterpret_cast<uint4*>(meet)[i] = uint4{0, 0, 0, 0};
   x += static_cast<size_t>(t0) * d;
   w_gate += static_cast<size_t>(e) * d;
   float acc[kRouteTokens] = {};
@@ -472,20 +489,25 @@ struct DecLayer {
     }
   }
 
+  // Rows r0 .. r0+4*RQ-1, summed over part `part` of `parts` of the (expert,
+  // chunk) list.  Where there are several parts their sums meet in memory and
+  // the workgroup that comes last adds them, in order.
   template <int RQ>
-  __device__ __forceinline__ void w2_rows(int r0) const {
+  __device__ __forceinline__ void w2_rows(int r0, int part, int parts) const {
     const int tid = threadIdx.x;
     // the (expert, chunk) list in equal units, as many for each wave, of at
     // least 16 chunks where there are enough
     const int C = (a.I + G::kChunk - 1) / G::kChunk;
-    const int items = uniform(sel.n) * C;
+    const int all = uniform(sel.n) * C;
+    const int first = static_cast<int>(static_cast<int64_t>(all) * part / parts);
+    const int items = static_cast<int>(static_cast<int64_t>(all) * (part + 1) / parts) - first;
     const int units = kWaves * min(max(items / (16 * kWaves), 1), kMany ? kSlots / kWaves : 4);
     for (int o = tid; o < units * kTok * 16; o += kThreads) (&red[0][0][0])[o] = 0.f;
     if (tid == 0) *ticket = 0;
     __syncthreads();
     for (int u = take(); u < units; u = take()) {
-      const int i1 = static_cast<int>(static_cast<int64_t>(items) * (u + 1) / units);
-      for (int it = static_cast<int>(static_cast<int64_t>(items) * u / units); it < i1;) {
+      const int i1 = first + static_cast<int>(static_cast<int64_t>(items) * (u + 1) / units);
+      for (int it = first + static_cast<int>(static_cast<int64_t>(items) * u / units); it < i1;) {
         const int i = it / C, c0 = it % C;
         const int c1 = min(C, c0 + i1 - it);
         w2_part<RQ>(u, i, r0, c0, c1);
@@ -497,99 +519,117 @@ struct DecLayer {
       const int t = o / (4 * RQ), r = o % (4 * RQ);
       float v = 0.f;
       for (int u = 0; u < units; ++u) v += red[u][t][r];
-      const size_t at = static_cast<size_t>(t) * a.d + r0 + r;
-      if constexpr (sizeof(AT) == 2) {
-        if (a.res) v += bf16_to_f32(static_cast<const bf16_t*>(a.res)[at]);
-        static_cast<bf16_t*>(a.out)[at] = f32_to_bf16(v);
-      } else {
-        if (a.res) v += static_cast<const float*>(a.res)[at];
-        static_cast<float*>(a.out)[at] = v;
-      }
+      if (parts == 1)
+        finish(v, t, r0 + r);
+      else
+        __hip_atomic_store(sums(r0 / 4, part) + o, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (parts > 1) {  // RQ == 1
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (tid == 0)
+        *ticket = __hip_atomic_fetch_add(dec_word(a, kDecCount + r0 / 4), 1, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      if (*ticket == parts - 1)
+        for (int o = tid; o < a.T * 4; o += kThreads) {
+          float v = 0.f;
+          for (int p = 0; p < parts; ++p)
+            v += __hip_atomic_load(sums(r0 / 4, p) + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          finish(v, o / 4, r0 + o % 4);
+        }
     }
     __syncthreads();  // the sums have been read
   }
 
+  __device__ __forceinline__ float* sums(int quad, int part) const {
+    const int w = part * (a.d / 4) + quad;  // the workgroup that holds them
+    return reinterpret_cast<float*>(a.meet + kDecMeetBytes) + w * (kDecodeMaxTokens * 4);
+  }
+
+  __device__ __forceinline__ void finish(float v, int t, int row) const {
+    const size_t at = static_cast<size_t>(t) * a.d + row;
+    if constexpr (sizeof(AT) == 2) {
+      if (a.res) v += bf16_to_f32(static_cast<const bf16_t*>(a.res)[at]);
+      static_cast<bf16_t*>(a.out)[at] = f32_to_bf16(v);
+    } else {
+      if (a.res) v += static_cast<const float*>(a.res)[at];
+      static_cast<float*>(a.out)[at] = v;
+    }
+  }
+
   __device__ void w2_share(int b) const {
     const int quads = a.d / 4;
+    if (2 * quads <= a.wgs) {
+      // fewer row quads than workgroups: several workgroups share one, each
+      // with at least eight chunks per wave
+      const int C = (a.I + G::kChunk - 1) / G::kChunk;
+      const int parts = max(min(a.wgs / quads, uniform(sel.n) * C / (8 * kWaves)), 1);
+      if (b < quads * parts) w2_rows<1>(4 * (b % quads), b / quads, parts);
+      return;
+    }
     const int q1 = static_cast<int>(static_cast<int64_t>(quads) * (b + 1) / a.wgs);
     int q = static_cast<int>(static_cast<int64_t>(quads) * b / a.wgs);
-    for (; q + 4 <= q1; q += 4) w2_rows<4>(4 * q);
+    for (; q + 4 <= q1; q += 4) w2_rows<4>(4 * q, 0, 1);
     switch (q1 - q) {
-      case 3: w2_rows<3>(4 * q); break;
-      case 2: w2_rows<2>(4 * q); break;
-      case 1: w2_rows<1>(4 * q); break;
+      case 3: w2_rows<3>(4 * q, 0, 1); break;
+      case 2: w2_rows<2>(4 * q, 0, 1); break;
+      case 1: w2_rows<1>(4 * q, 0, 1); break;
     }
   }
 };
 
 // The meeting between the halves.  A workgroup that has written its share sets
-// its flag and counts itself on its group's counter (every counter and go
-// word in a 128-byte line of its own: hundreds of workgroups polling or adding
-// to one line cost tens of microseconds); the last of a group counts the
-// group, the last group writes every group's go word, and a workgroup polls
-// only that of its own group.  The flags are read only by a workgroup that
-// has waited too long.
+// its flag.  Workgroup 0 polls the flags, a thread each, and writes the groups'
+// go words once all are set; the others poll their group's.  A workgroup that
+// has waited too long reads the flags itself.
 
 // Share b is out (every thread's stores of it are complete before the barrier).
-__device__ __forceinline__ void dec_publish(uint8_t* flags, int b) {
+__device__ __forceinline__ void dec_publish(const DecodeArgs& a, int b) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0)
-    __hip_atomic_store(flags + b, uint8_t(1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// Counts the workgroup (once, after publishing its own share).
-__device__ __forceinline__ void dec_arrive(const DecodeArgs& a) {
-  if (threadIdx.x != 0) return;
-  int32_t* words = reinterpret_cast<int32_t*>(a.flags + kDecMaxWgs);
-  auto line = [&](int i) { return words + i * (kDecLine / 4); };
-  const int groups = (a.wgs + kDecGroup - 1) / kDecGroup;
-  const int g = blockIdx.x / kDecGroup;
-  const int members = min(kDecGroup, a.wgs - g * kDecGroup);
-  if (__hip_atomic_fetch_add(line(g), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != members - 1)
-    return;
-  if (__hip_atomic_fetch_add(line(2 * kDecGroups), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) !=
-      groups - 1)
-    return;
-  for (int i = 0; i < groups; ++i)
-    __hip_atomic_store(line(kDecGroups + i), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0) dec_write(dec_word(a, kDecFlag + b), 1);
 }
 
 // Waits until every share is out (-1), or until `limit` ticks of the 100 MHz
 // clock have passed: then one whose flag is missing, the first from the
-// caller's own index on.
+// caller's own index on (-1 if none is by now).
 __device__ __forceinline__ int dec_wait(const DecodeArgs& a, int64_t limit, int* lds) {
   constexpr int kNone = 1 << 30;
-  if (threadIdx.x < 64) {
-    const int lane = threadIdx.x;
-    const int32_t* go = reinterpret_cast<const int32_t*>(a.flags + kDecMaxWgs) +
-                        (kDecGroups + blockIdx.x / kDecGroup) * (kDecLine / 4);
-    const int64_t start = wall_clock64();
-    int found = kNone;
-    while (!uniform(__hip_atomic_load(go, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))) {
-      if (wall_clock64() - start >= limit) {
-        int after = kNone, any = kNone;  // lowest missing: from blockIdx on, of all
-        for (int b = lane; b < a.wgs; b += 64)
-          if (!__hip_atomic_load(a.flags + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) {
-            any = min(any, b);
-            if (b >= static_cast<int>(blockIdx.x)) after = min(after, b);
-          }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-          any = min(any, __shfl_xor(any, off, 64));
-          after = min(after, __shfl_xor(after, off, 64));
-        }
-        found = after < kNone ? after : any;
-        break;
-      }
-      __builtin_amdgcn_s_sleep(1);
+  const int tid = threadIdx.x, me = blockIdx.x;
+  const int64_t start = wall_clock64();
+  bool done;
+  if (me == 0) {
+    bool late;
+    do {
+      done = __syncthreads_and(tid >= a.wgs || dec_read(dec_word(a, kDecFlag + tid)));
+      late = __syncthreads_or(tid == 0 && wall_clock64() - start >= limit);
+    } while (!done && !late);
+  } else {
+    if (tid < 64) {
+      const int32_t* go = dec_word(a, kDecGo + me / kDecGroup);
+      int set;
+      while (!(set = uniform(dec_read(go))) && wall_clock64() - start < limit)
+        __builtin_amdgcn_s_sleep(1);
+      if (tid == 0) *lds = set;
     }
-    if (lane == 0) *lds = found == kNone ? -1 : found;
+    __syncthreads();
+    done = *lds != 0;
+    __syncthreads();
   }
-  __syncthreads();
-  const int b = uniform(*lds);
-  __syncthreads();
-  return b;
+  int found = -1;
+  if (!done) {
+    if (tid == 0) *lds = kNone;
+    __syncthreads();
+    if (tid < a.wgs && !dec_read(dec_word(a, kDecFlag + tid)))
+      atomicMin(lds, (tid - me + a.wgs) % a.wgs);
+    __syncthreads();
+    const int missing = uniform(*lds);
+    __syncthreads();
+    if (missing != kNone) found = (missing + me) % a.wgs;
+  }
+  if (found < 0 && me == 0 && tid < kDecGroups) dec_write(dec_word(a, kDecGo + tid), 1);
+  return found;
 }
 
 template <typename WT, bool kMany>
@@ -615,8 +655,7 @@ decode_layer_kernel(DecodeArgs a, int phases) {
     for (int b = blockIdx.x; b >= 0;) {  // b is wave-uniform
       layer.w13_share(b);
       if (!(phases & 2)) return;
-      dec_publish(a.flags, b);
-      if (b == static_cast<int>(blockIdx.x)) dec_arrive(a);
+      dec_publish(a, b);
       b = dec_wait(a, limit, &next);
       limit = 0;
     }
@@ -633,13 +672,13 @@ decode_layer_kernel(DecodeArgs a, int phases) {
 
 int decode_workgroups(int cus) { return cus < kDecMaxWgs ? cus : kDecMaxWgs; }
 
-size_t decode_flag_bytes() { return kDecFlagBytes; }
+size_t decode_meet_bytes() { return kDecMeetBytes + kDecSumBytes; }
 
 template <typename AT>
 static hipError_t route(const DecodeArgs& a, hipStream_t s) {
   const dim3 grid(a.E, (a.T + kRouteTokens - 1) / kRouteTokens);
   decode_route_kernel<AT><<<grid, kRouteThreads, 0, s>>>(static_cast<const AT*>(a.x), a.w_gate,
-                                                         a.logits, a.flags, a.T, a.E, a.d);
+                                                         a.logits, a.meet, a.T, a.E, a.d);
   return hipGetLastError();
 }
 

@@ -268,7 +268,7 @@ struct DecodeArgs {
   void* out;            // [T, d]
   float* logits;        // [T, E] (workspace)
   void* h;              // [T*k, I] act dtype (workspace)
-  uint8_t* flags;       // decode_flag_bytes() (workspace), cleared by the route launch
+  uint8_t* meet;        // decode_meet_bytes() (workspace), cleared by the route launch
   int T, d, E, I, k;
   int wgs;              // workgroups of the layer launch
   int64_t wait_limit;   // 100 MHz ticks before a workgroup computes a missing share itself
@@ -276,7 +276,7 @@ struct DecodeArgs {
 
 // Workgroups of the layer launch that `cus` compute units hold at once.
 int decode_workgroups(int cus);
-size_t decode_flag_bytes();
+size_t decode_meet_bytes();
 hipError_t launch_decode_route(const DecodeArgs& a, hipStream_t s);
 // phases: 1 = W13, 2 = W2 and the sum over experts, 3 = both in one launch.
 hipError_t launch_decode_layer(const DecodeArgs& a, int phases, hipStream_t s);
