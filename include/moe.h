@@ -372,8 +372,9 @@ typedef struct moe_linear_desc {
   int32_t reserved;      /* must be 0                        */
 } moe_linear_desc;
 
-/* Bytes of device workspace moe_linear needs for `desc` (0 for most shapes:
- * only products whose K is split over workgroups use any). */
+/* Bytes of device workspace moe_linear needs for `desc`: 0 unless K is split
+ * over workgroups (few tiles) or rows that are not multiples of 16 bytes apart
+ * are worth copying first (more than four tokens). */
 MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* bytes);
 
 /* The product above on `stream`.  `scale` is required for e4m3fn weights and

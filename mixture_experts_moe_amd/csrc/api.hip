@@ -1006,7 +1006,7 @@ MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* byte
   const int st = check_linear(desc, &a);
   if (st) return st;
   if (!bytes) return MOE_ERR_NULL_PTR;
-  *bytes = moe::linear_part_bytes(a);
+  *bytes = a.M ? moe::linear_workspace(&a, nullptr) : 0;
   return MOE_OK;
 }
 
@@ -1022,11 +1022,10 @@ MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w
   if (scaled && !scale) return MOE_ERR_NULL_PTR;
   if (!scaled && scale) return MOE_ERR_BAD_DTYPE;
   if (!aligned16(scale) || !aligned16(bias) || !aligned16(residual)) return MOE_ERR_MISALIGNED;
-  const size_t need = moe::linear_part_bytes(a);
-  if (need) {
+  if (const size_t need = moe::linear_workspace(&a, nullptr)) {
     if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return MOE_ERR_MISALIGNED;
-    a.part = static_cast<float*>(workspace);
+    moe::linear_workspace(&a, workspace);
   }
   a.x = x;
   a.w = w;

@@ -243,12 +243,17 @@ struct LinearArgs {
   int tile;            // the kernel that runs (linear_plan)
   int splits;          // K ranges, each ksplit long (the last may be shorter)
   int ksplit;
+  bool pack_x, pack_w; // rows copied to the workspace first, kpack elements each
+  int kpack;
+  void* xpack;
+  void* wpack;
 };
 
 // Chooses the kernel and the K split (the other fields set, pointers not yet
 // needed).
 void linear_plan(LinearArgs* a);
-size_t linear_part_bytes(const LinearArgs& a);
+// The workspace a plan needs; sets its pointers into `ws` unless that is null.
+size_t linear_workspace(LinearArgs* a, void* ws);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------ few tokens

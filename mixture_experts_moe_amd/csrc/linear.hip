@@ -1082,6 +1082,43 @@ __global__ __launch_bounds__(kLinStreamThreads, RT > 1 ? 2 : 4) void linear_stre
   }
 }
 
+// ------------------------------------------------------------ packing
+//
+// Rows that do not start at multiples of 16 bytes cannot go through the
+// direct-to-LDS loads; where the product is large enough to pay for it they
+// are copied into the workspace first, each row to a multiple of 16 bytes and
+// zero past its end.  A thread makes one 16-byte unit of x or of W.
+
+constexpr int kPackThreads = 256;
+template <typename WT>
+__global__ __launch_bounds__(kPackThreads) void linear_pack_kernel(LinearArgs a) {
+  using AT = typename StreamTypes<WT>::AT;
+  constexpr int xn = 16 / (int)sizeof(AT), wn = 16 / (int)sizeof(WT);
+  const int64_t xu = a.pack_x ? a.kpack / xn : 0, wu = a.pack_w ? a.kpack / wn : 0;
+  int64_t o = static_cast<int64_t>(blockIdx.x) * kPackThreads + threadIdx.x;
+  if (o < a.M * xu) {
+    const AT* row = static_cast<const AT*>(a.x) + o / xu * a.ldx;
+    static_cast<u32x4*>(a.xpack)[o] = lin_unit<AT>(row, static_cast<int>(o % xu) * xn, a.K);
+    return;
+  }
+  o -= a.M * xu;
+  if (o < a.R * wu) {
+    const WT* row = static_cast<const WT*>(a.w) + o / wu * a.ldw;
+    static_cast<u32x4*>(a.wpack)[o] = lin_unit<WT>(row, static_cast<int>(o % wu) * wn, a.K);
+  }
+}
+
+template <typename WT>
+static hipError_t launch_pack(LinearArgs* a, hipStream_t s) {
+  const int64_t units = (a->pack_x ? a->M * a->kpack / (16 / (int)sizeof(typename StreamTypes<WT>::AT)) : 0) +
+                        (a->pack_w ? a->R * static_cast<int64_t>(a->kpack) / (16 / (int)sizeof(WT)) : 0);
+  linear_pack_kernel<WT><<<static_cast<unsigned>((units + kPackThreads - 1) / kPackThreads),
+                           kPackThreads, 0, s>>>(*a);
+  if (a->pack_x) a->x = a->xpack, a->ldx = a->kpack;
+  if (a->pack_w) a->w = a->wpack, a->ldw = a->kpack;
+  return hipGetLastError();
+}
+
 // ------------------------------------------------------------ launchers
 
 template <typename WT, int RT, bool kQuads, bool kGated>
@@ -1195,18 +1232,9 @@ constexpr TileCost kTileCosts[] = {
 constexpr int kComputeUnits = 256;
 constexpr float kUsPerKb = 0.017f;
 
-static bool linear_aligned(const LinearArgs& a) {
-  const int esz = a.w_dtype == kDtypeE4M3FN ? 16 : a.w_dtype == kDtypeBF16 ? 8 : 4;
-  const int xsz = a.act_dtype == kDtypeF32 ? 4 : 8;
-  return a.ldw % esz == 0 && a.ldx % xsz == 0 && a.K % esz == 0;
-}
-
-void linear_plan(LinearArgs* a) {
-  a->splits = 1;
-  a->ksplit = a->K;
-  a->tile = kTileStream;
-  if (a->M <= kLinStreamTokens) return;
-  const bool aligned = linear_aligned(*a);
+// The tile and K ranges of the least estimated time among the aligned tiles
+// or the staged ones: that time, and the choice in *a.
+static float linear_choose(LinearArgs* a, bool aligned) {
   const int wb = a->w_dtype == kDtypeE4M3FN ? 1 : a->w_dtype == kDtypeBF16 ? 2 : 4;
   const int kc = wb == 4 ? 32 : 64;
   const float bytes = static_cast<float>(a->R) * a->K * wb +
@@ -1214,33 +1242,30 @@ void linear_plan(LinearArgs* a) {
   float best = 1e30f;
   for (const TileCost& t : kTileCosts) {
     if (aligned != (t.tile < kTileStaged128)) continue;
-    const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) *
-                          ((a->R + t.rows - 1) / t.rows);
+    const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) * ((a->R + t.rows - 1) / t.rows);
     const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
     // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
     const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f * 1.1f;
     const int waves = t.tile == kTile64 || t.tile == kTileStaged64 ? 4 : 8;
     int held = 160 / t.lds_kb[wb == 1];
     if (held > 16 / waves) held = 16 / waves;
-    for (int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       // ranges of whole stage pairs, of at least four stages
       const int per = ((a->K + want - 1) / want + 2 * kc - 1) / (2 * kc) * (2 * kc);
       if (want > 1 && per < 4 * kc) break;
       const int splits = (a->K + per - 1) / per;
       const float stages = static_cast<float>((per + kc - 1) / kc);
-      int64_t left = (tiles * splits + kComputeUnits - 1) / kComputeUnits;  // per unit
-      const int64_t rounds = left / held;
+      const int64_t here = (tiles * splits + kComputeUnits - 1) / kComputeUnits;  // per unit
       auto round_us = [&](int n) {
         float stage = t.fixed + kUsPerKb * kb;
         if (n * kUsPerKb * kb > stage) stage = n * kUsPerKb * kb;
         if (n * mfma > stage) stage = n * mfma;
         return stages * stage + t.start;
       };
-      float us = rounds * round_us(held);
-      if (left % held) us += round_us(static_cast<int>(left % held));
+      float us = (here / held) * round_us(held);
+      if (here % held) us += round_us(static_cast<int>(here % held));
       if (us < bytes / 4.7e6f) us = bytes / 4.7e6f;
-      if (splits > 1)
-        us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 5.2e6f;
+      if (splits > 1) us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 5.2e6f;
       if (us < best) {
         best = us;
         a->tile = t.tile;
@@ -1249,15 +1274,65 @@ void linear_plan(LinearArgs* a) {
       }
     }
   }
+  return best;
 }
 
-size_t linear_part_bytes(const LinearArgs& a) {
+void linear_plan(LinearArgs* a) {
+  const int wsz = a->w_dtype == kDtypeE4M3FN ? 1 : a->w_dtype == kDtypeBF16 ? 2 : 4;
+  const int xsz = a->act_dtype == kDtypeF32 ? 4 : 2;
+  const bool w_ok = a->ldw * wsz % 16 == 0 && a->K * wsz % 16 == 0;
+  const bool x_ok = a->ldx * xsz % 16 == 0 && a->K * xsz % 16 == 0;
+  a->splits = 1;
+  a->ksplit = a->K;
+  a->tile = kTileStream;
+  a->pack_x = a->pack_w = false;
+  a->kpack = (a->K * wsz + 15) / 16 * 16 / wsz;
+  if (a->M <= kLinStreamTokens) {
+    // a few unaligned tokens cost less to copy than W costs to read unaligned
+    a->pack_x = a->M > 4 && w_ok && !x_ok;
+    return;
+  }
+  if (w_ok && x_ok) {
+    linear_choose(a, true);
+    return;
+  }
+  LinearArgs packed = *a;
+  packed.pack_x = !x_ok || !w_ok;  // K must be padded in both
+  packed.pack_w = !w_ok;
+  float us = linear_choose(&packed, true) + 2.5f;
+  us += 2.f * static_cast<float>(a->M) * a->K * xsz / 4e6f;
+  if (packed.pack_w) us += 2.f * static_cast<float>(a->R) * a->K * wsz / 4e6f;
+  if (us < linear_choose(a, false)) *a = packed;
+}
+
+// Workspace: the K ranges' sums, packed x, packed W.
+static size_t part_bytes(const LinearArgs& a) {
   return a.splits > 1 ? static_cast<size_t>(a.splits) * a.M * a.R * 4 : 0;
+}
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t linear_workspace(LinearArgs* a, void* ws) {
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    void* p = ws && n ? static_cast<char*>(ws) + at : nullptr;
+    at += up256(n);
+    return p;
+  };
+  const int wsz = a->w_dtype == kDtypeE4M3FN ? 1 : a->w_dtype == kDtypeBF16 ? 2 : 4;
+  a->part = static_cast<float*>(take(part_bytes(*a)));
+  a->xpack = take(a->pack_x ? static_cast<size_t>(a->M) * a->kpack * (a->act_dtype == kDtypeF32 ? 4 : 2) : 0);
+  a->wpack = take(a->pack_w ? static_cast<size_t>(a->R) * a->kpack * wsz : 0);
+  return at;
 }
 
 template <typename WT>
-static hipError_t launch_type(const LinearArgs& a, hipStream_t s) {
+static hipError_t launch_type(LinearArgs a, hipStream_t s) {
   hipError_t e = hipErrorInvalidValue;
+  if (a.pack_x || a.pack_w) {
+    e = launch_pack<WT>(&a, s);
+    if (e != hipSuccess) return e;
+    if (a.pack_w) a.K = a.kpack;  // zeros in both operands past the row
+  }
   switch (a.tile) {
     case kTileStream: return launch_stream<WT>(a, s);
     case kTile256: e = launch_pp<WT>(a, s); break;

@@ -345,22 +345,30 @@ struct Stream16 {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
-  __device__ __forceinline__ void direct(int c, f32x4 (&acc)[RT]) const {
-    Toks x;
-    u32x4 w[kUnits][RT];
+  // N chunks straight to registers: all their loads, then their MFMAs.
+  template <int N>
+  __device__ __forceinline__ void direct(int c0, int step, f32x4 (&acc)[RT]) const {
+    Toks x[N];
+    u32x4 w[N][kUnits][RT];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u)
+    for (int p = 0; p < N; ++p) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        w[u][t] = reinterpret_cast<const StreamUnit*>(
-                      lane_row(t) + static_cast<size_t>(c) * kWStep + wo[t][0] + 64 * u)
-                      ->v;
-    load_x(x, c);
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          w[p][u][t] = reinterpret_cast<const StreamUnit*>(
+                           lane_row(t) + static_cast<size_t>(c0 + p * step) * kWStep + wo[t][0] +
+                           64 * u)
+                           ->v;
+      load_x(x[p], c0 + p * step);
+    }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u)
+    for (int p = 0; p < N; ++p)
 #pragma unroll
-      for (int t = 0; t < RT; ++t) acc[t] = mma(w[u][t], x[u], acc[t]);
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] = mma(w[p][u][t], x[p][u], acc[t]);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -387,7 +395,8 @@ struct Stream16 {
         use<kLoadCount>(1, x1, acc);
       }
     } else {
-      for (; n >= 1; --n, c0 += step) direct(c0, acc);
+      for (; n >= 2; n -= 2, c0 += 2 * step) direct<2>(c0, step, acc);
+      if (n >= 1) direct<1>(c0, step, acc);
     }
   }
 
