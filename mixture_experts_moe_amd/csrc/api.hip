@@ -997,6 +997,7 @@ static int check_linear(const moe_linear_desc* d, LinearArgs* a) {
   a->gated = d->gated != 0;
   a->scale_channel = d->scale_mode == MOE_SCALE_PER_CHANNEL;
   a->vec4 = a->ldo % 4 == 0 && a->ldr % 4 == 0;  // the buffers are 16-byte aligned
+  a->vec8 = a->ldo % 8 == 0 && a->ldr % 8 == 0;
   moe::linear_plan(a);
   return MOE_OK;
 }

@@ -239,7 +239,7 @@ struct LinearArgs {
   int64_t ldx, ldw, ldr, ldo;  // elements
   int act_dtype, w_dtype, fn;
   bool gated, scale_channel;
-  bool vec4;           // out (and residual) rows hold aligned vectors of four
+  bool vec4, vec8;     // out (and residual) rows hold aligned vectors of four, eight
   int tile;            // the kernel that runs (linear_plan)
   int splits;          // K ranges, each ksplit long (the last may be shorter)
   int ksplit;

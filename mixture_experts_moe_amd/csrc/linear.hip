@@ -28,12 +28,33 @@ __device__ __forceinline__ float lin_sigmoid_times(float z, float u) {  // z / (
   return z / (1.0f + expf(-u));
 }
 
+// z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2.  For bf16 results Phi's tail is
+// e^(-z^2/2) P(t), t = 1 / (1 + 0.38 |z| / sqrt 2), P of degree 7: a minimax fit
+// of e^(x^2) erfc(x) / 2 over 0 <= x <= 12 whose relative error is 1.1e-6, so the
+// tail keeps its relative accuracy down to where it leaves the type's range.  It
+// is short enough to stand in the epilogue once per value (802 x 13400 x 2888 bf16:
+// erfcf, one copy in a loop, 98 us; this 79).
+template <bool kFast>
+__device__ __forceinline__ float lin_gelu(float z) {
+  if constexpr (!kFast) return 0.5f * z * erfcf(z * -0.70710678118654752f);
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.26870057685088805f * fabsf(z));
+  float p = -0.0627079869797211f;
+  p = p * t + 0.16801539047659845f;
+  p = p * t - 0.03495267354882652f;
+  p = p * t + 0.12391424436400950f;
+  p = p * t + 0.09029839441786437f;
+  p = p * t + 0.10828843519853950f;
+  p = p * t + 0.10714368014064054f;
+  const float q = p * t * __expf(-0.5f * z * z);
+  return z * (z < 0.f ? q : 1.0f - q);
+}
+
 template <bool kFast>
 __device__ __forceinline__ float lin_act(int fn, float z) {
   switch (fn) {
     case kFnRelu: return z < 0.f ? 0.f : z;  // NaN stays
     case kFnSilu: return lin_sigmoid_times<kFast>(z, z);
-    case kFnGelu: return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case kFnGelu: return lin_gelu<kFast>(z);
     case kFnGeluTanh:  // tanh(u) = 2 / (1 + e^-2u) - 1, u = sqrt(2/pi) (z + 0.044715 z^3)
       return lin_sigmoid_times<kFast>(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
   }
@@ -117,7 +138,12 @@ struct LinQuad {
       case kFnRelu: apply(kFnRelu); break;
       case kFnSilu: apply(kFnSilu); break;
       case kFnGeluTanh: apply(kFnGeluTanh); break;
-      case kFnGelu:  // a long function: one copy
+      case kFnGelu:
+        if constexpr (sizeof(AT) == 2) {
+          apply(kFnGelu);
+          break;
+        }
+        // a long function in fp32: one copy
 #pragma unroll 1
         for (int i = 0; i < 4 * kRows; ++i) {
           float z = zg[0][0];
@@ -175,6 +201,166 @@ struct LinQuad {
         p[v] = zg[v];
         if (kGated) p[a.N + v] = zu[v];
       }
+  }
+};
+
+// Eight consecutive channels n .. n+7 (those below N): scales and biases read
+// once, then any number of tokens.
+template <typename AT, bool kGated>
+struct LinOct {
+  float sg[8], su[8], bg[8], bu[8];
+  int n, valid;  // channels that exist
+
+  __device__ __forceinline__ void init(const LinearArgs& a, int n_) {
+    n = n_;
+    valid = min(a.N - n, 8);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int c = min(n + v, a.N - 1);
+      sg[v] = !a.scale ? 1.f : a.scale[a.scale_channel ? c : 0];
+      bg[v] = a.bias ? a.bias[c] : 0.f;
+      if (kGated) {
+        su[v] = !a.scale ? 1.f : a.scale[a.scale_channel ? a.N + c : 0];
+        bu[v] = a.bias ? a.bias[a.N + c] : 0.f;
+      }
+    }
+  }
+
+  // One token's channel sums zg (zu: the up half's) -> out[m, n ..].
+  __device__ __forceinline__ void finish(const LinearArgs& a, float (&zg)[8], float (&zu)[8],
+                                         int64_t m) const {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      zg[v] = zg[v] * sg[v] + bg[v];
+      if (kGated) zu[v] = zu[v] * su[v] + bu[v];
+    }
+    auto apply = [&](int fn) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) zg[v] = lin_act<sizeof(AT) == 2>(fn, zg[v]);
+    };
+    switch (a.fn) {
+      case kFnRelu: apply(kFnRelu); break;
+      case kFnSilu: apply(kFnSilu); break;
+      case kFnGeluTanh: apply(kFnGeluTanh); break;
+      case kFnGelu:
+        if constexpr (sizeof(AT) == 2) {
+          apply(kFnGelu);
+          break;
+        }
+        // a long function in fp32: one copy
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          float z = zg[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) z = i == j ? zg[j] : z;
+          z = lin_act<sizeof(AT) == 2>(kFnGelu, z);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) zg[j] = i == j ? z : zg[j];
+        }
+        break;
+    }
+    if (kGated) {
+#pragma unroll
+      for (int v = 0; v < 8; ++v) zg[v] *= zu[v];
+    }
+    AT* o = static_cast<AT*>(a.out) + m * a.ldo + n;
+    const AT* r = static_cast<const AT*>(a.res) + m * a.ldr + n;
+    if (a.vec8 && valid == 8) {
+      constexpr int kParts = sizeof(AT) == 4 ? 2 : 1;  // 16-byte pieces
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        if constexpr (sizeof(AT) == 4) {
+          f32x4 z{zg[4 * p], zg[4 * p + 1], zg[4 * p + 2], zg[4 * p + 3]};
+          if (a.res) z += reinterpret_cast<const f32x4*>(r)[p];
+          reinterpret_cast<f32x4*>(o)[p] = z;
+        } else {
+          if (a.res) {
+            const uint4 q = *reinterpret_cast<const uint4*>(r);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              zg[2 * i] += __uint_as_float(w[i] << 16);
+              zg[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
+          // the hardware's conversion: to nearest even, NaN kept
+          bf16x8 h;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = static_cast<__bf16>(zg[i]);
+          *reinterpret_cast<bf16x8*>(o) = h;
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      if (v < valid) lin_store(o + v, a.res ? zg[v] + lin_load(r + v) : zg[v]);
+  }
+
+  // the sums of this K range instead, where K is split
+  __device__ __forceinline__ void store_part(const LinearArgs& a, const float (&zg)[8],
+                                             const float (&zu)[8], int64_t m) const {
+    float* p = a.part + (static_cast<size_t>(blockIdx.z) * a.M + m) * a.R + n;
+#pragma unroll
+    for (int h = 0; h < (kGated ? 2 : 1); ++h) {
+      const float* z = h ? zu : zg;
+      float* q = p + (h ? a.N : 0);
+      if (a.N % 4 == 0) {
+#pragma unroll
+        for (int v = 0; v < 8; v += 4)
+          if (v < valid) *reinterpret_cast<f32x4*>(q + v) = f32x4{z[v], z[v + 1], z[v + 2], z[v + 3]};
+      } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          if (v < valid) q[v] = z[v];
+      }
+    }
+  }
+};
+
+// A wave's tile on its way out: its sums go through LDS of its own (2 KB per
+// 64 rows), eight tokens at a time, so that a lane finishes eight consecutive
+// channels of one token and the wave stores whole lines; the epilogue is one
+// short loop whatever the tile.  kRW: weight rows of the wave (gated: gate
+// rows, then up rows).
+template <typename AT, bool kGated, int kRW>
+struct LinOut {
+  static constexpr int kC = kGated ? kRW / 2 : kRW;  // channels
+  static constexpr int kLanes = kC / 8;              // of a token
+  static constexpr int kBytes = 8 * kRW * 4;
+  LinOct<AT, kGated> oct;
+  f32x4* lds;  // [8 tokens][kRW / 4], units swizzled by the token
+
+  // The channel of the lane's first output among the wave's kC.
+  static __device__ __forceinline__ int lane_channel() {
+    return (threadIdx.x & 63) % kLanes * 8;
+  }
+  // four sums of rows 4q .. 4q+3 for token t
+  __device__ __forceinline__ void put(int t, int q, f32x4 v) const {
+    lds[t * (kRW / 4) + (q ^ (t & 7))] = v;
+  }
+  // tokens m0 .. m0+7
+  __device__ __forceinline__ void flush(const LinearArgs& a, int64_t m0) const {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int lane = threadIdx.x & 63, q = lane % kLanes * 2;
+#pragma unroll
+    for (int it = 0; it < (8 * kLanes + 63) / 64; ++it) {
+      const int t = it * (64 / kLanes) + lane / kLanes;
+      if (t >= 8 || m0 + t >= a.M || oct.valid <= 0) continue;
+      float zg[8], zu[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4 g = lds[t * (kRW / 4) + ((q + h) ^ (t & 7))];
+        const f32x4 u = kGated ? lds[t * (kRW / 4) + ((kC / 4 + q + h) ^ (t & 7))] : g;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) zg[4 * h + v] = g[v], zu[4 * h + v] = u[v];
+      }
+      if (a.part)
+        oct.store_part(a, zg, zu, m0 + t);
+      else
+        oct.finish(a, zg, zu, m0 + t);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 };
 
@@ -648,45 +834,6 @@ __device__ __forceinline__ bool lin_raster(int p, int gx, int gy, int cols, int*
   return true;
 }
 
-// A wave's sums of 32 tokens into rows of `sums`.
-template <typename WT>
-__device__ __forceinline__ void pp_put(f32x4 (*sums)[64], const PpAcc<WT>& a0, const PpAcc<WT>& a1,
-                                       int wm, int r16, int g) {
-#pragma unroll
-  for (int u = 0; u < PpTypes<WT>::kX; ++u)
-#pragma unroll
-    for (int t = 0; t < PpTypes<WT>::kW; ++t) {
-      sums[16 * u + r16][(16 * wm + 4 * t + g) ^ r16] = a0[t][u];
-      sums[16 * u + r16][(32 + 16 * wm + 4 * t + g) ^ r16] = a1[t][u];
-    }
-}
-
-// Finishes the 32 tokens from m0 on held in `sums`: a thread takes the same
-// four channels of every 8th (gated: 16th) token.
-template <typename AT, bool kGated, int kCh>
-__device__ __forceinline__ void pp_finish(const LinearArgs& a, const f32x4 (*sums)[64],
-                                          const LinQuad<AT, kGated>& quad, int64_t m0) {
-  constexpr int kQuads = kCh / 4, kStep = kPpThreads / kQuads, kRows = 32 / kStep;
-  const int q = threadIdx.x % kQuads, row0 = threadIdx.x / kQuads;
-  f32x4 zg[kRows], zu[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i * kStep;
-    zg[i] = sums[row][q ^ (row & 15)];
-    zu[i] = kGated ? sums[row][(kQuads + q) ^ (row & 15)] : zg[i];
-  }
-  if (a.part) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      if (m0 + row0 + i * kStep < a.M) quad.store_part(a, zg[i], zu[i], m0 + row0 + i * kStep);
-    return;
-  }
-  quad.template values<kRows>(a, zg, zu);
-#pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (m0 + row0 + i * kStep < a.M) quad.store(a, zg[i], m0 + row0 + i * kStep);
-}
-
 template <typename WT, bool kGated>
 __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, int gx, int gy) {
   using P = PpTypes<WT>;
@@ -695,7 +842,7 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
   constexpr int kWP = kPpPiece * P::kWRow, kXP = kPpPiece * 128;
   __shared__ __attribute__((aligned(1024))) uint8_t w00[kWP], w01[kWP], x00[kXP], x01[kXP];
   __shared__ __attribute__((aligned(1024))) uint8_t w10[kWP], w11[kWP], x10[kXP], x11[kXP];
-  __shared__ __attribute__((aligned(1024))) f32x4 sums[32][64];
+  __shared__ __attribute__((aligned(1024))) uint8_t sums[8][4096];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kCh = kGated ? kPpPiece : 2 * kPpPiece;  // channels of a tile
@@ -754,25 +901,27 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
   tile.template stage<1, 2>(w10, w11, x10, x11, nullptr, 0, f, acc);
   if (!late) pp_barrier();
 
-  // The sums leave through LDS, 32 tokens (the two waves of one wn) at a
-  // time, so that every wave finishes and stores whole rows and the epilogue
-  // is one short loop.  A row is the tile's 256 sums of a token, its 16-byte
-  // units swizzled by the token.
+  // 128 weight rows of the wave: 64 of each piece (gated: 64 gate, 64 up)
+  using Out = LinOut<AT, kGated, 128>;
+  Out out;
+  out.lds = reinterpret_cast<f32x4*>(sums[wave]);
+  const int c = Out::lane_channel();
+  out.oct.init(a, n0 + 64 * wm + c + (!kGated && c >= 64 ? 64 : 0));
   const int r16 = lane & 15, g = lane >> 4;
-  LinQuad<AT, kGated> quad;
-  const int nq = n0 + 4 * static_cast<int>(threadIdx.x % (kCh / 4));
-  if (nq < a.N) quad.init(a, nq);
 #pragma unroll 1
-  for (int r = 0; r < 8; ++r) {
-    __syncthreads();
-    if (wn == (r & 3)) {
-      if (r < 4)
-        pp_put<WT>(sums, acc[0][0], acc[1][0], wm, r16, g);
-      else
-        pp_put<WT>(sums, acc[0][1], acc[1][1], wm, r16, g);
+  for (int h = 0; h < 8; ++h) {  // eight tokens of token tile u = h / 2 % 2, column j = h / 4
+    if (r16 / 8 == h % 2) {
+#pragma unroll
+      for (int ju = 0; ju < 4; ++ju)
+        if (h / 2 == ju) {
+#pragma unroll
+          for (int t = 0; t < P::kW; ++t) {
+            out.put(r16 & 7, 4 * t + g, acc[0][ju / 2][t][ju % 2]);
+            out.put(r16 & 7, 16 + 4 * t + g, acc[1][ju / 2][t][ju % 2]);
+          }
+        }
     }
-    __syncthreads();
-    if (nq < a.N) pp_finish<AT, kGated, kCh>(a, sums, quad, m0 + 32 * r);
+    out.flush(a, m0 + 128 * (h / 4) + 32 * wn + 8 * (h % 4));
   }
 }
 
