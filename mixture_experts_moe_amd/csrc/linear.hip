@@ -1363,20 +1363,23 @@ enum LinearTile { kTileStream, kTile256, kTile128, kTile128Pair, kTile128x64, kT
 
 struct TileCost {
   int tile, rows, tokens;
+  int types;      // weight bytes that it is built for, or'ed
   int lds_kb[2];  // stages in LDS: with weights of two or four bytes, of one
   float fixed;    // us per stage apart from the bytes
   float start;    // us per workgroup: first loads and epilogue
 };
-// the aligned tiles, then the staged ones
+// the aligned tiles, then the staged ones (a tile is not built for types whose
+// every size has a cheaper one: fp32 is bound by its MFMAs in any tile, and
+// e4m3fn's stages are small enough to hold two workgroups or four stages)
 constexpr TileCost kTileCosts[] = {
-    {kTile256, 256, 256, {160, 128}, 0.27f, 11.f},
-    {kTile128, 128, 128, {128, 96}, 0.27f, 1.f},
-    {kTile128Pair, 128, 128, {64, 48}, 0.27f, 1.f},
-    {kTile128x64, 128, 64, {96, 64}, 0.27f, 1.f},
-    {kTile128x64Pair, 128, 64, {72, 48}, 0.27f, 1.f},
-    {kTile64, 64, 64, {64, 48}, 0.25f, 0.5f},
-    {kTileStaged128, 128, 128, {32, 24}, 1.2f, 1.f},
-    {kTileStaged64, 64, 64, {16, 12}, 0.7f, 1.f},
+    {kTile256, 256, 256, 1 | 2, {160, 128}, 0.27f, 11.f},
+    {kTile128, 128, 128, 2 | 4, {128, 96}, 0.27f, 1.f},
+    {kTile128Pair, 128, 128, 1 | 2 | 4, {64, 48}, 0.27f, 1.f},
+    {kTile128x64, 128, 64, 1 | 2, {96, 64}, 0.27f, 1.f},
+    {kTile128x64Pair, 128, 64, 2 | 4, {72, 48}, 0.27f, 1.f},
+    {kTile64, 64, 64, 1 | 2 | 4, {64, 48}, 0.25f, 0.5f},
+    {kTileStaged128, 128, 128, 1 | 2 | 4, {32, 24}, 1.2f, 1.f},
+    {kTileStaged64, 64, 64, 1 | 2 | 4, {16, 12}, 0.7f, 1.f},
 };
 constexpr int kComputeUnits = 256;
 constexpr float kUsPerKb = 0.017f;
@@ -1390,7 +1393,7 @@ static float linear_choose(LinearArgs* a, bool aligned) {
                       static_cast<float>(a->M) * (a->K + a->N) * (wb == 4 ? 4 : 2);
   float best = 1e30f;
   for (const TileCost& t : kTileCosts) {
-    if (aligned != (t.tile < kTileStaged128)) continue;
+    if (!(t.types & wb) || aligned != (t.tile < kTileStaged128)) continue;
     const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) * ((a->R + t.rows - 1) / t.rows);
     const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
     // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
@@ -1484,13 +1487,21 @@ static hipError_t launch_type(LinearArgs a, hipStream_t s) {
   }
   switch (a.tile) {
     case kTileStream: return launch_stream<WT>(a, s);
-    case kTile256: e = launch_pp<WT>(a, s); break;
+    case kTile256:
+      if constexpr (sizeof(WT) != 4) e = launch_pp<WT>(a, s);
+      break;
     // a ring of four stages alone on its compute unit, or less LDS and two
     // workgroups side by side
-    case kTile128: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 4>(a, s); break;
+    case kTile128:
+      if constexpr (sizeof(WT) != 1) e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 4>(a, s);
+      break;
     case kTile128Pair: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 2>(a, s); break;
-    case kTile128x64: e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 4>(a, s); break;
-    case kTile128x64Pair: e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 3>(a, s); break;
+    case kTile128x64:
+      if constexpr (sizeof(WT) != 4) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 4>(a, s);
+      break;
+    case kTile128x64Pair:
+      if constexpr (sizeof(WT) != 1) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 3>(a, s);
+      break;
     case kTile64: e = launch_tile<WT, LinGeom<WT, 2, 2, 2, 2>, 4>(a, s); break;
     case kTileStaged128: e = launch_staged<WT, LinGeom<WT, 2, 4, 4, 2>>(a, s); break;
     case kTileStaged64: e = launch_staged<WT, LinGeom<WT, 2, 2, 2, 2>>(a, s); break;

@@ -64,9 +64,9 @@ def reference(inp, residual=None):
     return out, tol, usable
 
 
-def check(got, inp, residual=None):
+def check(got, inp, residual=None, least=0.8):
     want, tol, usable = reference(inp, residual)
-    assert usable.float().mean() > 0.8
+    assert usable.float().mean() > least
     assert torch.isfinite(got.float()).all()
     err = (got.double() - want).abs()[usable]
     worst = float((err / tol[usable]).max())
@@ -102,6 +102,24 @@ def test_values(T, d, E, k, I, w):
     inp = layer(T, d, E, k, I, w)
     res = rand_like(inp.x) if T % 2 else None
     check(decode(inp, residual=res), inp, res)
+
+
+@pytest.mark.parametrize("w", ["f32", "bf16", "e4m3fn"])
+@pytest.mark.parametrize("T,d,E,k,I", [(1, 7168, 4, 2, 128), (4, 5120, 8, 2, 192),
+                                       (13, 7168, 6, 3, 64), (16, 8192, 4, 1, 128),
+                                       (2, 4160, 16, 4, 64)])
+def test_more_output_rows_than_four_per_unit(T, d, E, k, I, w):
+    """Workgroups with several groups of four rows of W2, evenly and not.
+
+    The bound on a logit's error grows with d squared: (2d + 64) 2^-24 of
+    sum |x||w| = 0.032 d, twice 0.2 at d = 7168, while a logit's deviation is
+    0.05 sqrt(d) = 4.2 and the kept and the first dropped of six lie about 1.2
+    apart: about a third of the tokens are left out, more than the fifth that
+    the smaller layers allow.
+    """
+    print(f"decode wide T={T} d={d} E={E} k={k} I={I} {w}", flush=True)
+    inp = layer(T, d, E, k, I, w)
+    check(decode(inp), inp, least=0.3)
 
 
 @pytest.mark.parametrize("T", range(1, 17))

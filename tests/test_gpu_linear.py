@@ -102,6 +102,71 @@ def test_values(M, N, K, gated, fmt):
     check(out, x, w, fn, gated, b, scale, r)
 
 
+# Larger products: every tile size with whole and split K, tiles that end past
+# M and N, K that ends inside a stage, and rows that are copied to be aligned
+# (K not a multiple of 16 bytes).
+LARGE = [("bf16", 975, 12755, 720, False), ("bf16", 422, 13115, 736, True),
+         ("bf16", 129, 10887, 7328, False), ("bf16", 139, 6384, 4976, True),
+         ("bf16", 1310, 8982, 802, False), ("bf16", 901, 6272, 670, True),
+         ("bf16", 1452, 1869, 6279, False), ("e4m3fn", 3302, 4264, 1040, False),
+         ("e4m3fn", 2977, 1397, 1568, True), ("e4m3fn", 147, 14600, 8176, False),
+         ("e4m3fn", 986, 10000, 1813, False), ("e4m3fn", 770, 3175, 7162, True),
+         ("bf16", 459, 4097, 64, False), ("bf16", 73, 11581, 64, True),
+         ("bf16", 68, 1458, 5712, False), ("bf16", 1738, 2320, 72, False),
+         ("bf16", 307, 6585, 64, True), ("bf16", 1954, 133, 5376, False),
+         ("bf16", 65, 2998, 2640, True), ("bf16", 42, 15235, 496, True),
+         ("bf16", 21, 10198, 1840, False), ("bf16", 5386, 694, 240, False),
+         ("bf16", 167, 9540, 64, True), ("bf16", 22, 8468, 2528, True),
+         ("bf16", 998, 4305, 82, False), ("bf16", 138, 12673, 67, True),
+         ("bf16", 72, 4765, 4897, False), ("bf16", 2660, 3356, 70, False),
+         ("e4m3fn", 238, 8849, 64, True), ("e4m3fn", 5617, 179, 2848, False),
+         ("e4m3fn", 1118, 2836, 64, False), ("e4m3fn", 20, 5305, 1184, True),
+         ("e4m3fn", 1097, 1954, 710, False), ("e4m3fn", 217, 8283, 67, True),
+         ("e4m3fn", 96, 12901, 3078, False), ("f32", 197, 12707, 64, False),
+         ("f32", 67, 4606, 528, True), ("f32", 962, 3901, 64, True),
+         ("f32", 2075, 211, 7616, False), ("f32", 284, 12322, 68, False),
+         ("f32", 19, 9381, 544, True), ("f32", 328, 8656, 69, False),
+         ("f32", 71, 3071, 607, True), ("f32", 26, 65, 155, False)]
+
+
+@pytest.mark.parametrize("fmt,M,N,K,gated", LARGE)
+def test_large_products(M, N, K, gated, fmt):
+    print(f"linear large {M}x{N}x{K} gated={gated} {fmt}", flush=True)
+    fn = FNS[(M + N + K) % len(FNS)]
+    x, w, b, scale, r = inputs(M, N, K, fmt, gated, bias=(N + K) % 3 > 0, residual=M % 2 > 0)
+    out = B.moe_linear(x, w, bias=b, activation=fn, gated=gated, scale=scale, residual=r)
+    check(out, x, w, fn, gated, b, scale, r)
+
+
+@pytest.mark.parametrize("xpad,wpad", [(3, 0), (0, 3)])
+@pytest.mark.parametrize("M,N,K", [(2, 300, 512), (6, 520, 512), (16, 96, 1024), (600, 2100, 520),
+                                   (1300, 4200, 328)])
+def test_one_operand_of_unaligned_rows(M, N, K, xpad, wpad):
+    x, w, b, _, r = inputs(M, N, K, "bf16")
+    _, xv = padded(x, xpad, float("nan"))
+    _, wv = padded(w, wpad, float("nan"))
+    out = B.moe_linear(xv, wv, bias=b, activation="relu", residual=r)
+    check(out, x, w, "relu", False, b, None, r)
+
+
+def test_operands_beyond_32_bit_offsets():
+    """Rows 2^20 elements apart, more than 2^32 elements after the first."""
+    M, N, K, ld = 4200, 136, 64, 1 << 20
+    x, w, b, _, r = inputs(M, N, K, "bf16")
+    xb = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    xb[:, :K] = x
+    ob = torch.empty((M, ld), dtype=torch.bfloat16, device="cuda")
+    out = B.moe_linear(xb[:, :K], w, bias=b, residual=r, out=ob[:, :N])
+    check(out, x, w, None, False, b, None, r)
+    del xb, ob
+    wb = torch.empty((2 * M, ld), dtype=torch.bfloat16, device="cuda")
+    for m in (3, 70):
+        x, w, b, _, r = inputs(m, M, K, "bf16", gated=True)
+        wb[:, :K] = w
+        out = B.moe_linear(x, wb[:, :K], bias=b, gated=True, residual=r)
+        check(out, x, w, None, True, b, None, r)
+
+
 @pytest.mark.parametrize("fn", FNS)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("M", [4, 40])
@@ -175,7 +240,7 @@ def test_out_may_be_the_residual(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 2048), (16, 640, 4096), (48, 256, 8192),
-                                   (300, 520, 1024)])
+                                   (300, 520, 1024), (1800, 4100, 999), (2048, 4096, 1024)])
 def test_same_bits_every_time_and_in_a_graph(M, N, K):
     x, w, b, _, r = inputs(M, N, K, "bf16")
     want = B.moe_linear(x, w, bias=b, residual=r)
