@@ -552,14 +552,14 @@ def _one_gpu(*ts: Optional[torch.Tensor]) -> int:
     return index
 
 
-def _allocator(dev: torch.device, index: int, stream):
-    """(hipStream_t, allocate(shape, dtype)): tensors belong to the launch
+def _allocator(x: torch.Tensor, index: int, stream):
+    """(hipStream_t, allocate(shape, dtype=x's)): tensors belong to the launch
     stream, which torch's allocator takes without a stream switch where it is
-    the current one."""
-    current = torch.cuda.current_stream(index)
-    if stream is None or stream == current:
-        return current.cuda_stream, lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
-    return stream.cuda_stream, lambda shape, dtype: _alloc(shape, dtype, dev, stream)
+    the current one of x's device."""
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or stream.cuda_stream == current:
+        return current, x.new_empty
+    return stream.cuda_stream, lambda shape, dtype=x.dtype: _alloc(shape, dtype, x.device, stream)
 
 
 class _Here:
@@ -601,18 +601,20 @@ def moe_decode(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: tor
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError(f"residual must match x in shape and dtype: residual "
                          f"{tuple(residual.shape)} {residual.dtype}, x {tuple(x.shape)} {x.dtype}")
-    _dev(x, w_gate, w13, w2, residual, out)
-    index = x.get_device()
+    given = (x, w_gate, w13, w2, residual, out)
+    index = _one_gpu(*given)
+    if not all(t is None or t.is_contiguous() for t in given):
+        raise ValueError("all tensors must be contiguous")
     desc = make_desc(T, d, E, I, _act_code(x), _w_code(w13), 0, None, schedule)
     ref = ctypes.byref(desc)
     sc = _scales(w13, scales)
-    s, new = _allocator(x.device, index, stream)
+    s, new = _allocator(x, index, stream)
     if out is None:
-        out = new((T, d), x.dtype)
+        out = new((T, d))
     nbytes = ctypes.c_size_t()
     _check("moe_decode_workspace_bytes",
            lib().moe_decode_workspace_bytes(ref, int(top_k), nbytes))
-    ws = workspace if workspace is not None else new((max(nbytes.value, 1),), torch.uint8)
+    ws = workspace if workspace is not None else new((max(nbytes.value, 1),), dtype=torch.uint8)
     if ws.numel() * ws.element_size() < nbytes.value:
         raise ValueError("workspace too small")
     with _on(index):
@@ -687,14 +689,14 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
     desc = moe_linear_desc(M, N, K, ldx, ldw, ldr, ldo, act, wdt, _FNS[activation],
                            1 if gated else 0, mode, 0)
     ref = ctypes.byref(desc)
-    s, new = _allocator(x.device, index, stream)
+    s, new = _allocator(x, index, stream)
     if out is None:
-        out = new((M, N), x.dtype)
+        out = new((M, N))
     nbytes = ctypes.c_size_t()
     _check("moe_linear_workspace_bytes", lib().moe_linear_workspace_bytes(ref, nbytes))
     ws = None
     if nbytes.value:
-        ws = workspace if workspace is not None else new((nbytes.value,), torch.uint8)
+        ws = workspace if workspace is not None else new((nbytes.value,), dtype=torch.uint8)
         if ws.numel() * ws.element_size() < nbytes.value:
             raise ValueError("workspace too small")
     with _on(index):
