@@ -382,8 +382,9 @@ MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* byte
  * itself (same address and row stride); otherwise out overlaps no input.
  * The elements of out's rows past N are left as they are.  `workspace`:
  * moe_linear_workspace_bytes(desc) bytes, 256-byte aligned (may be NULL when
- * that is 0).  The result does not depend on what else runs, nor on the run:
- * every sum has a fixed order.  Kernel timing (moe_timing_enable) covers the
+ * that is 0), of its own for every call that may overlap another.  The result
+ * does not depend on what else runs, nor on the run: every sum has a fixed
+ * order.  Capturable into a graph.  Kernel timing (moe_timing_enable) covers the
  * layer's kernels, not this one. */
 MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
                        const float* scale, const float* bias, const void* residual, void* out,

@@ -580,6 +580,19 @@ def _on(index: int):
     return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
+def _ws(workspace: Optional[torch.Tensor], nbytes: int, index: int, new) -> torch.Tensor:
+    """The caller's workspace if it will do, or a new one."""
+    if workspace is None:
+        return new((nbytes,), dtype=torch.uint8)
+    if _one_gpu(workspace) != index:
+        raise ValueError("workspace must be on the tensors' device")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return workspace
+
+
 def moe_decode_workspace_bytes(desc: moe_desc, top_k: int) -> int:
     n = ctypes.c_size_t()
     _check("moe_decode_workspace_bytes",
@@ -614,9 +627,7 @@ def moe_decode(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: tor
     nbytes = ctypes.c_size_t()
     _check("moe_decode_workspace_bytes",
            lib().moe_decode_workspace_bytes(ref, int(top_k), nbytes))
-    ws = workspace if workspace is not None else new((max(nbytes.value, 1),), dtype=torch.uint8)
-    if ws.numel() * ws.element_size() < nbytes.value:
-        raise ValueError("workspace too small")
+    ws = _ws(workspace, max(nbytes.value, 1), index, new)
     with _on(index):
         _check("moe_decode", lib().moe_decode(
             ref, x.data_ptr(), w_gate.data_ptr(), w13.data_ptr(), w2.data_ptr(), int(top_k),
@@ -636,7 +647,11 @@ def _rows(name: str, t: torch.Tensor, shape) -> int:
     ld, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} must have dense rows, got strides {(ld, step)}")
-    return ld if rows > 1 else cols
+    if rows <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap: strides {(ld, step)} for {list(shape)}")
+    return ld
 
 
 def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
@@ -694,11 +709,7 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
         out = new((M, N))
     nbytes = ctypes.c_size_t()
     _check("moe_linear_workspace_bytes", lib().moe_linear_workspace_bytes(ref, nbytes))
-    ws = None
-    if nbytes.value:
-        ws = workspace if workspace is not None else new((nbytes.value,), dtype=torch.uint8)
-        if ws.numel() * ws.element_size() < nbytes.value:
-            raise ValueError("workspace too small")
+    ws = _ws(workspace, nbytes.value, index, new) if nbytes.value else None
     with _on(index):
         _check("moe_linear", lib().moe_linear(
             ref, x.data_ptr(), w.data_ptr(), _addr(scale), _addr(bias), _addr(residual),

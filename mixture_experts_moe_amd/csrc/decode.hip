@@ -1,23 +1,25 @@
 // The whole MoE layer for at most 16 tokens in two launches.
 //
-//   1. decode_route_kernel: logits = x . W_gate^T (fp32), a workgroup per few
-//      experts; it also clears the flags below.
+//   1. decode_route_kernel: logits = x . W_gate^T (fp32), a workgroup per
+//      expert and four tokens; it also clears the words that the next
+//      launch's workgroups meet through.
 //   2. decode_layer_kernel: every workgroup selects the experts from the
 //      logits by itself (a few hundred values, cheaper than another launch),
 //      computes its share of h = SiLU(W1 x) * (W3 x), publishes it, and then
 //      its share of the output channels: out = residual + sum_j gate_j W2 h_j,
 //      all experts of a channel in one workgroup, so nothing is added up
-//      through memory.
+//      through memory (but where there are fewer than two channel quads per
+//      workgroup several share one, see w2_share).
 //
 // With so few tokens the layer is a read of the selected experts' weights:
 // each is read exactly once (stream.h), whatever the number of its tokens.
 //
 // Between the two halves every workgroup needs every other's h.  Each
 // workgroup has a flag of its own, written once its h rows are out at device
-// scope, and reads all of them.  No workgroup depends on another one being
-// resident: one that finds a share missing for longer than the limit computes
-// that share itself (the same bits, to the same place), so every wait ends
-// whatever else the GPU runs.
+// scope; workgroup 0 reads them all and tells the others, a word for 32 of
+// them.  No workgroup depends on another one being resident: one that finds a
+// share missing for longer than the limit computes that share itself (the
+// same bits, to the same place), so every wait ends whatever else the GPU runs.
 
 #include "kernels.h"
 #include "stream.h"
@@ -261,7 +263,6 @@ __device__ __forceinline__ void dec_select(const float* logits, int T, int E, in
 }
 
 // ------------------------------------------------------------ the layer
-
 
 // kMany: more than four tokens in the call; experts with up to four of them
 // take the 4x4 MFMAs, the others the 16x16 (stream.h).

@@ -1170,7 +1170,8 @@ constexpr int kLinStreamWaves = kLinStreamThreads / 64;
 // kQuads: at most four tokens, 4x4 MFMAs, else 16x16 (RT tiles of 16 rows;
 // gated: eight gate rows, then eight up rows).
 template <typename WT, int RT, bool kQuads, bool kGated, bool kAligned>
-__global__ __launch_bounds__(kLinStreamThreads, RT > 1 ? 2 : 4) void linear_stream_kernel(LinearArgs a) {
+__global__ __launch_bounds__(kLinStreamThreads, RT > 1 ? 2 : 4) void linear_stream_kernel(
+    LinearArgs a) {
   using G = StreamGeom<WT>;
   using AT = typename G::AT;
   using S16 = Stream16<WT, RT, kAligned>;
@@ -1296,8 +1297,9 @@ __global__ __launch_bounds__(kPackThreads) void linear_pack_kernel(LinearArgs a)
 
 template <typename WT>
 static hipError_t launch_pack(LinearArgs* a, hipStream_t s) {
-  const int64_t units = (a->pack_x ? a->M * a->kpack / (16 / (int)sizeof(typename StreamTypes<WT>::AT)) : 0) +
-                        (a->pack_w ? a->R * static_cast<int64_t>(a->kpack) / (16 / (int)sizeof(WT)) : 0);
+  constexpr int xn = 16 / (int)sizeof(typename StreamTypes<WT>::AT), wn = 16 / (int)sizeof(WT);
+  const int64_t units = (a->pack_x ? a->M * (a->kpack / xn) : 0) +
+                        (a->pack_w ? static_cast<int64_t>(a->R) * (a->kpack / wn) : 0);
   linear_pack_kernel<WT><<<static_cast<unsigned>((units + kPackThreads - 1) / kPackThreads),
                            kPackThreads, 0, s>>>(*a);
   if (a->pack_x) a->x = a->xpack, a->ldx = a->kpack;
@@ -1322,11 +1324,18 @@ static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
 
 template <typename WT, bool kGated>
 static hipError_t launch_stream(const LinearArgs& a, hipStream_t s) {
+  // (4 x 4096 x 4096 bf16: 4x4 MFMAs 8.6 us, 16x16 10.2; 4 x 28672 x 4096
+  // e4m3fn 28.7, 36.6)
   if (a.M <= 4) return launch_stream<WT, 1, true, kGated>(a, s);
-  // e4m3fn weights are half the bytes of their tokens, so two tiles sharing
-  // each token load pay as long as the grid still fills the chip.
+  // More 16-row tiles than compute units but fewer than two each leave some
+  // with twice the work of others; e4m3fn weights are half the bytes of their
+  // tokens, so two tiles per workgroup, sharing each token load, are faster
+  // there (16 x 4500 x 7168: 20.5 us with one, 15.9 with two; 8 x 7168 x 4096
+  // 12.7, 12.4) and slower elsewhere (8 x 4096 x 4096: 8.6, 10.1; 8 x 28672 x
+  // 4096: 33.8, 38.2).
   if constexpr (sizeof(WT) == 1) {
-    if (a.R >= 6144) return launch_stream<WT, 2, false, kGated>(a, s);
+    const int tiles = (a.R + 15) / 16;
+    if (tiles > 256 && tiles < 512) return launch_stream<WT, 2, false, kGated>(a, s);
   }
   return launch_stream<WT, 1, false, kGated>(a, s);
 }
@@ -1491,7 +1500,9 @@ void linear_plan(LinearArgs* a) {
   float us = linear_choose(&packed, true) + 2.5f;
   us += 2.f * static_cast<float>(a->M) * a->K * xsz / 4e6f;
   if (packed.pack_w) us += 2.f * static_cast<float>(a->R) * a->K * wsz / 4e6f;
-  if (us < linear_choose(a, false)) *a = packed;
+  // (a launch of at most 2^32 threads)
+  const bool fits = (static_cast<int64_t>(a->R) * wsz + a->M * xsz) * a->kpack < int64_t{1} << 35;
+  if (us < linear_choose(a, false) && fits) *a = packed;
 }
 
 // Workspace: the K ranges' sums, packed x, packed W.
@@ -1509,7 +1520,8 @@ size_t linear_workspace(LinearArgs* a, void* ws) {
   };
   const int wsz = a->w_dtype == kDtypeE4M3FN ? 1 : a->w_dtype == kDtypeBF16 ? 2 : 4;
   a->part = static_cast<float*>(take(part_bytes(*a)));
-  a->xpack = take(a->pack_x ? static_cast<size_t>(a->M) * a->kpack * (a->act_dtype == kDtypeF32 ? 4 : 2) : 0);
+  const int xsz = a->act_dtype == kDtypeF32 ? 4 : 2;
+  a->xpack = take(a->pack_x ? static_cast<size_t>(a->M) * a->kpack * xsz : 0);
   a->wpack = take(a->pack_w ? static_cast<size_t>(a->R) * a->kpack * wsz : 0);
   return at;
 }

@@ -260,3 +260,16 @@ def test_with_a_shared_expert(T, w):
 def test_no_tokens():
     inp = layer(1, 64, 2, 1, 64, "bf16")
     assert B.moe_decode(inp.x[:0], inp.w_gate, inp.w13, inp.w2, 1).shape == (0, 64)
+
+
+def test_workspaces_that_will_not_do_are_refused():
+    inp = layer(3, 128, 8, 2, 64, "bf16")
+    want = decode(inp)
+    n = B.moe_decode_workspace_bytes(B.make_desc(3, 128, 8, 64, B.MOE_DTYPE_BF16, B.MOE_DTYPE_BF16), 2)
+    for ws in (torch.empty(n, dtype=torch.uint8),
+               torch.empty(n - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)):
+        with pytest.raises(ValueError):
+            decode(inp, workspace=ws)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert torch.equal(decode(inp, workspace=ws), want)

@@ -11,6 +11,7 @@ have slopes of at most 1.13 (gated: the product rule), are themselves good to
 step, eps/2 of its magnitude.
 """
 
+import ctypes
 import math
 
 import pytest
@@ -281,3 +282,28 @@ def test_two_streams_with_their_own_workspaces():
 def test_no_tokens():
     x, w, b, _, r = inputs(4, 64, 64, "bf16")
     assert B.moe_linear(x[:0], w, bias=b, residual=r[:0]).shape == (0, 64)
+
+
+def test_workspaces_that_will_not_do_are_refused():
+    x, w, _, _, _ = inputs(48, 256, 8192, "bf16")           # K is split
+    desc = B.moe_linear_desc(48, 256, 8192, 0, 0, 0, 0, B.MOE_DTYPE_BF16, B.MOE_DTYPE_BF16, 0, 0, 0, 0)
+    n = ctypes.c_size_t()
+    assert B.lib().moe_linear_workspace_bytes(ctypes.byref(desc), n) == 0 and n.value > 0
+    for ws in (torch.empty(n.value, dtype=torch.uint8),
+               torch.empty(n.value - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(1, dtype=torch.uint8, device="cuda").expand(n.value)):
+        with pytest.raises(ValueError):
+            B.moe_linear(x, w, workspace=ws)
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    assert torch.equal(B.moe_linear(x, w, workspace=ws), B.moe_linear(x, w))
+
+
+def test_one_row_of_a_wider_matrix():
+    """One row (and one column) may have any stride."""
+    x, w, b, _, _ = inputs(1, 40, 64, "f32")
+    out = B.moe_linear(x.expand(1, 64), w, bias=b)
+    check(out, x, w, None, False, b, None, None)
+    x, w, b, _, _ = inputs(30, 40, 1, "f32")
+    wide = torch.randn((30, 7), device="cuda")
+    wide[:, :1] = x
+    check(B.moe_linear(wide[:, :1], w, bias=b), x, w, None, False, b, None, None)

@@ -104,3 +104,18 @@ def test_binding_checks(lib, exc, match, kw):
     args.update(kw)
     with pytest.raises(exc, match=match):
         B.moe_linear(args.pop("x"), args.pop("w"), **args)
+
+
+def test_rows_that_overlap_are_refused():
+    """A stride shorter than the row (an expanded row has 0) would be read as dense."""
+    x, w = torch.zeros(1, 64), torch.zeros(8, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        B.moe_linear(x.expand(20, 64), w)
+    with pytest.raises(ValueError, match="overlap"):
+        B.moe_linear(torch.zeros(20, 64), w[:1].expand(8, 64))
+    with pytest.raises(ValueError, match="overlap"):
+        B.moe_linear(torch.zeros(100).as_strided((4, 64), (8, 1)), w)
+    with pytest.raises(ValueError, match="overlap"):
+        B.moe_linear(torch.zeros(20, 64), w, residual=torch.zeros(1, 8).expand(20, 8))
+    with pytest.raises(ValueError, match="overlap"):
+        B.moe_linear(torch.zeros(20, 64), w, out=torch.zeros(1, 8).expand(20, 8))
