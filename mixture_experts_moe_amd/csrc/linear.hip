@@ -432,8 +432,14 @@ using LinAcc = f32x4[G::TA][G::TB];
 // acc += W_rows . X_rows^T over one stage.  wrow(t), xrow(u): LDS rows of
 // this lane's 16-row tiles.
 template <typename WT, class G>
-__device__ __forceinline__ void lin_mma(const uint8_t* stage, const int (&wrow)[G::TA],
-                                        const int (&xrow)[G::TB], LinAcc<G>& acc) {
+struct LinFrags {
+  static constexpr int kW = sizeof(WT) == 1 ? 1 : 2;  // 16-byte units per lane and weight tile
+  uint4 w[kW][G::TA], x[2][G::TB];
+};
+
+template <typename WT, class G>
+__device__ __forceinline__ void lin_read(LinFrags<WT, G>& f, const uint8_t* stage,
+                                         const int (&wrow)[G::TA], const int (&xrow)[G::TB]) {
   const uint8_t* ws = stage;
   const uint8_t* xs = stage + G::kWBytes;
   const int g = (threadIdx.x & 63) >> 4;
@@ -445,39 +451,42 @@ __device__ __forceinline__ void lin_mma(const uint8_t* stage, const int (&wrow)[
     return *reinterpret_cast<const uint4*>(xs + xrow[u] * G::kXRow +
                                            ((s ^ lin_swz<G::kXRow>(xrow[u])) << 4));
   };
-  if constexpr (sizeof(WT) == 1) {
-    // a lane's 16 codes k = 16g .. 16g+15: the first eight in one MFMA, the
-    // last eight in the next, against the token units of the same k
-    uint4 x0[G::TB], x1[G::TB];
+  constexpr int kW = LinFrags<WT, G>::kW;
 #pragma unroll
-    for (int u = 0; u < G::TB; ++u) {
-      x0[u] = xunit(u, 2 * g);
-      x1[u] = xunit(u, 2 * g + 1);
-    }
+  for (int h = 0; h < 2; ++h) {
+    if (h < kW)
+#pragma unroll
+      for (int t = 0; t < G::TA; ++t) f.w[h][t] = wunit(t, 4 * h + g);
+    // e4m3fn: a lane's 16 codes are k = 16g .. 16g+15, so its token units are
+    // those of the same k
+#pragma unroll
+    for (int u = 0; u < G::TB; ++u) f.x[h][u] = xunit(u, kW == 1 ? 2 * g + h : 4 * h + g);
+  }
+}
+
+template <typename WT, class G>
+__device__ __forceinline__ void lin_mma(const LinFrags<WT, G>& f, LinAcc<G>& acc) {
+  if constexpr (sizeof(WT) == 1) {
+    // the first eight codes in one MFMA, the last eight in the next
 #pragma unroll
     for (int t = 0; t < G::TA; ++t) {
-      const uint4 q = wunit(t, g);
+      const uint4 q = f.w[0][t];
       const bf16x8 lo = as_frag(e4m3x8_to_frag_bits(q.x, q.y));
       const bf16x8 hi = as_frag(e4m3x8_to_frag_bits(q.z, q.w));
 #pragma unroll
-      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(lo, as_frag(x0[u]), acc[t][u]);
+      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(lo, as_frag(f.x[0][u]), acc[t][u]);
 #pragma unroll
-      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(hi, as_frag(x1[u]), acc[t][u]);
+      for (int u = 0; u < G::TB; ++u) acc[t][u] = mfma16x16x32(hi, as_frag(f.x[1][u]), acc[t][u]);
     }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint4 wf[G::TA], xf[G::TB];
-#pragma unroll
-      for (int t = 0; t < G::TA; ++t) wf[t] = wunit(t, 4 * h + g);
-#pragma unroll
-      for (int u = 0; u < G::TB; ++u) xf[u] = xunit(u, 4 * h + g);
       if constexpr (sizeof(WT) == 2) {
 #pragma unroll
         for (int t = 0; t < G::TA; ++t)
 #pragma unroll
           for (int u = 0; u < G::TB; ++u)
-            acc[t][u] = mfma16x16x32(as_frag(wf[t]), as_frag(xf[u]), acc[t][u]);
+            acc[t][u] = mfma16x16x32(as_frag(f.w[h][t]), as_frag(f.x[h][u]), acc[t][u]);
       } else {
         // MFMA i takes element i of every lane group's four k
 #pragma unroll
@@ -486,8 +495,8 @@ __device__ __forceinline__ void lin_mma(const uint8_t* stage, const int (&wrow)[
           for (int t = 0; t < G::TA; ++t)
 #pragma unroll
             for (int u = 0; u < G::TB; ++u)
-              acc[t][u] = mfma16x16x4f32(__builtin_bit_cast(f32x4, wf[t])[i],
-                                         __builtin_bit_cast(f32x4, xf[u])[i], acc[t][u]);
+              acc[t][u] = mfma16x16x4f32(__builtin_bit_cast(f32x4, f.w[h][t])[i],
+                                         __builtin_bit_cast(f32x4, f.x[h][u])[i], acc[t][u]);
       }
     }
   }
@@ -627,7 +636,9 @@ __global__ __launch_bounds__(G::kThreads) void linear_staged_kernel(LinearArgs a
       *reinterpret_cast<u32x4*>(stage + G::kWBytes + 16 * (q * G::kThreads + tid)) = xv[q];
     __syncthreads();
     if (k0 + G::kKC < k_end) fetch(k0 + G::kKC);  // in flight during the MFMAs
-    lin_mma<WT, G>(stage, wrow, xrow, acc);
+    LinFrags<WT, G> f;
+    lin_read<WT, G>(f, stage, wrow, xrow);
+    lin_mma<WT, G>(f, acc);
   }
   lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
 }
@@ -1009,13 +1020,43 @@ struct TileLoader {
   }
 };
 
+// f(LinInt<A>), ..., f(LinInt<B - 1>)
+template <int I>
+struct LinInt {
+  static constexpr int value = I;
+};
+template <int A, int B, class F>
+__device__ __forceinline__ void lin_for(const F& f) {
+  if constexpr (A < B) {
+    f(LinInt<A>{});
+    lin_for<A + 1, B>(f);
+  }
+}
+
 template <typename WT, class G, int S, bool kGated>
 __global__ __launch_bounds__(G::kThreads) void linear_tile_kernel(LinearArgs a, int gx, int gy) {
   using AT = typename G::AT;
-  static_assert(S >= 2 && S <= 4, "ring depth");
+  // A workgroup that is alone on its compute unit reads a stage's fragments
+  // while it multiplies the one before (512 x 7168 x 4096 bf16, 128 x 128:
+  // 59.6 -> 51.3 us); two that take turns need not, and their 128 registers
+  // hold no second set.  64 x 64 tiles gain 2% and, short as their products
+  // are, lose as much to the longer start.
+  constexpr bool kAhead = S > 3 && G::TN > 64;
+  static_assert(S >= 2 && S <= 6 && (S % 2 == 0 || !kAhead), "ring depth");
   constexpr int kCh = kGated ? G::TN / 2 : G::TN;
+  // arrays of their own: reads of one stage wait for no load into another
   __shared__ __attribute__((aligned(1024))) uint8_t s0[G::kStage], s1[G::kStage],
-      s2[S > 2 ? G::kStage : 16], s3[S > 3 ? G::kStage : 16];
+      s2[S > 2 ? G::kStage : 16], s3[S > 3 ? G::kStage : 16], s4[S > 4 ? G::kStage : 16],
+      s5[S > 5 ? G::kStage : 16];
+  auto ring = [&](auto i) -> uint8_t* {
+    constexpr int k = decltype(i)::value % S;
+    if constexpr (k == 0) return s0;
+    if constexpr (k == 1) return s1;
+    if constexpr (k == 2) return s2;
+    if constexpr (k == 3) return s3;
+    if constexpr (k == 4) return s4;
+    if constexpr (k == 5) return s5;
+  };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tx, ty;
@@ -1051,79 +1092,58 @@ __global__ __launch_bounds__(G::kThreads) void linear_tile_kernel(LinearArgs a, 
     lw.issue(st, k_begin + i * G::kKC, k_end);
     lx.issue(st + G::kWBytes, k_begin + i * G::kKC, k_end);
   };
-  // stage i, in `cur`; `prev` held stage i - 1, which everybody has read once
-  // past the barrier
-  auto step = [&](uint8_t* cur, uint8_t* prev, int i) {
-    if (i + S - 1 < nst) {
-      pp_wait_loads<L * (S - 2)>();
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      issue(prev, i + S - 1);
-    } else {
-      pp_wait_loads<0>();
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    lin_mma<WT, G>(cur, wrow, xrow, acc);
-  };
-  // the first stages go so that the last one is in the ring's last buffer and
-  // whole turns follow: stage i in buffer (i + first) % S
+  // Stage i is in buffer (i + first) % S: the last one is in the ring's last
+  // buffer, so that whole turns follow the first, shortened one.
   const int first = (S - nst % S) % S;
-  int i = 0;
-  if constexpr (S == 2) {
-    if (first == 0) {
-      issue(s0, 0);
-    } else {
-      issue(s1, 0);
-      step(s1, s0, 0);
-      i = 1;
-    }
-    for (; i < nst; i += 2) {
-      step(s0, s1, i);
-      step(s1, s0, i + 1);
-    }
-  } else if constexpr (S == 3) {
-    if (first == 0) {
-      issue(s0, 0), issue(s1, 1);
-    } else if (first == 1) {
-      issue(s1, 0), issue(s2, 1);
-      step(s1, s0, 0), step(s2, s1, 1);
-      i = 2;
-    } else {
-      issue(s2, 0);
-      if (nst > 1) issue(s0, 1);
-      step(s2, s1, 0);
-      i = 1;
-    }
-    for (; i < nst; i += 3) {
-      step(s0, s2, i);
-      step(s1, s0, i + 1);
-      step(s2, s1, i + 2);
-    }
-  } else {
-    if (first == 0) {
-      issue(s0, 0), issue(s1, 1), issue(s2, 2);
-    } else if (first == 1) {
-      issue(s1, 0), issue(s2, 1), issue(s3, 2);
-      step(s1, s0, 0), step(s2, s1, 1), step(s3, s2, 2);
-      i = 3;
-    } else if (first == 2) {
-      issue(s2, 0), issue(s3, 1);
-      if (nst > 2) issue(s0, 2);
-      step(s2, s1, 0), step(s3, s2, 1);
-      i = 2;
-    } else {
-      issue(s3, 0);
-      if (nst > 1) issue(s0, 1), issue(s1, 2);
-      step(s3, s2, 0);
-      i = 1;
-    }
-    for (; i < nst; i += 4) {
-      step(s0, s3, i);
-      step(s1, s0, i + 1);
-      step(s2, s1, i + 2);
-      step(s3, s2, i + 3);
-    }
+  constexpr int kFirst = kAhead ? S : S - 1;  // stages issued before the first is used
+  lin_for<0, 2 * S - 1>([&](auto j) {         // in order
+    const int i = j.value - first;
+    if (i >= 0 && i < kFirst && i < nst) issue(ring(j), i);
+  });
+  LinFrags<WT, G> f[kAhead ? 2 : 1];
+  if constexpr (kAhead) {
+    if (nst >= S)
+      pp_wait_loads<L * (S - 1)>();
+    else
+      pp_wait_loads<0>();
+    asm volatile("s_barrier" ::: "memory");
+    lin_for<0, S>([&](auto j) {
+      if (j.value == first) lin_read<WT, G>(f[j.value % 2], ring(j), wrow, xrow);
+    });
   }
+  for (int turn = -first; turn < nst; turn += S)
+    lin_for<0, S>([&](auto j) {
+      constexpr int J = decltype(j)::value;
+      const int i = turn + J;
+      if (i < 0) return;  // uniform
+      if constexpr (kAhead) {
+        if (i + S < nst) {
+          pp_wait_loads<L * (S - 2)>();  // stage i + 1 has landed
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          issue(ring(j), i + S);  // every wave has read stage i
+        } else if (J + 1 < S) {
+          pp_wait_loads<L * (J + 2 < S ? S - 2 - J : 0)>();
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // (after the last stage, of a buffer whose contents mean nothing)
+        lin_read<WT, G>(f[(J + 1) % 2], ring(LinInt<J + 1>{}), wrow, xrow);
+        __builtin_amdgcn_sched_barrier(0);
+        lin_mma<WT, G>(f[J % 2], acc);
+      } else {
+        if (i + S - 1 < nst) {
+          pp_wait_loads<L * (S - 2)>();  // stage i has landed
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          issue(ring(LinInt<J + S - 1>{}), i + S - 1);  // every wave has read stage i - 1
+        } else {
+          pp_wait_loads<0>();
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        lin_read<WT, G>(f[0], ring(j), wrow, xrow);
+        lin_mma<WT, G>(f[0], acc);
+      }
+    });
   lin_epilogue<WT, G, kGated>(a, acc, m0, n0, wn, wm);
 }
 
@@ -1401,8 +1421,9 @@ static hipError_t launch_staged(const LinearArgs& a, hipStream_t s) {
 // rounds of as many as a compute unit's LDS holds.  Split sums are written
 // and read once more.  The constants were fitted to the tiles' times alone
 // and side by side (one workgroup per unit: 128 x 128 0.81 us a stage, 64 x 64
-// 0.54; the 256 x 256 tile 1.08); over 17..1024 tokens x 512..28672 rows x
-// 512..4096 K the choice measured within 12% of the best.
+// 0.54; the 256 x 256 tile 1.08).  Of every tile with one to three K ranges
+// the choice measured within 12% of the best at 20 sizes of 64..3305 tokens x
+// 2000..28672 rows x 80..8192 K in bf16 and e4m3fn.
 
 enum LinearTile { kTileStream, kTile256, kTile128, kTile128Pair, kTile128x64, kTile128x64Pair,
                   kTile64, kTileStaged128, kTileStaged64 };
@@ -1421,7 +1442,7 @@ constexpr TileCost kTileCosts[] = {
     {kTile256, 256, 256, 1 | 2, {160, 128}, 0.27f, 11.f},
     {kTile128, 128, 128, 2 | 4, {128, 96}, 0.27f, 1.f},
     {kTile128Pair, 128, 128, 1 | 2 | 4, {64, 48}, 0.27f, 1.f},
-    {kTile128x64, 128, 64, 1 | 2, {96, 64}, 0.27f, 1.f},
+    {kTile128x64, 128, 64, 1 | 2, {144, 64}, 0.27f, 1.f},
     {kTile128x64Pair, 128, 64, 2 | 4, {72, 48}, 0.27f, 1.f},
     {kTile64, 64, 64, 1 | 2 | 4, {64, 48}, 0.25f, 0.5f},
     {kTileStaged128, 128, 128, 1 | 2 | 4, {32, 24}, 1.2f, 1.f},
@@ -1443,8 +1464,10 @@ static float linear_choose(LinearArgs* a, bool aligned) {
     const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) * ((a->R + t.rows - 1) / t.rows);
     const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
     // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
-    const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f * 1.1f;
-    const int waves = t.tile == kTile64 || t.tile == kTileStaged64 ? 4 : 8;
+    // (staged tiles overlap them with little else)
+    const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f *
+                       (aligned ? 1.1f : 1.6f);
+    const int waves = t.rows == 64 ? 4 : 8;
     int held = 160 / t.lds_kb[wb == 1];
     if (held > 16 / waves) held = 16 / waves;
     for (int want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
@@ -1463,7 +1486,7 @@ static float linear_choose(LinearArgs* a, bool aligned) {
       float us = (here / held) * round_us(held);
       if (here % held) us += round_us(static_cast<int>(here % held));
       if (us < bytes / 4.7e6f) us = bytes / 4.7e6f;
-      if (splits > 1) us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 5.2e6f;
+      if (splits > 1) us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 3e6f;
       if (us < best) {
         best = us;
         a->tile = t.tile;
@@ -1546,7 +1569,7 @@ static hipError_t launch_type(LinearArgs a, hipStream_t s) {
       break;
     case kTile128Pair: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 2>(a, s); break;
     case kTile128x64:
-      if constexpr (sizeof(WT) != 4) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 4>(a, s);
+      if constexpr (sizeof(WT) != 4) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, sizeof(WT) == 1 ? 4 : 6>(a, s);
       break;
     case kTile128x64Pair:
       if constexpr (sizeof(WT) != 1) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 3>(a, s);
