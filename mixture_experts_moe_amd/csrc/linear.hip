@@ -1466,9 +1466,10 @@ static float linear_choose(LinearArgs* a, bool aligned) {
     const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) * ((a->R + t.rows - 1) / t.rows);
     const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
     // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
-    // (staged tiles overlap them with little else)
+    // (fp32's are all of a stage and leave gaps between stages; staged tiles
+    // overlap them with little else)
     const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f *
-                       (aligned ? 1.1f : 1.6f);
+                       (!aligned ? 1.6f : wb == 4 ? 1.35f : 1.1f);
     const int waves = t.rows == 64 ? 4 : 8;
     int held = 160 / t.lds_kb[wb == 1];
     if (held > 16 / waves) held = 16 / waves;
