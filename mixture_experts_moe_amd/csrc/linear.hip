@@ -5,7 +5,7 @@
 //
 // The product is computed transposed, as in the expert kernels: weight rows
 // (output channels) on the 16-row side of the MFMA and tokens on its columns,
-// so a lane ends with four consecutive channels of one token.
+// so a lane ends with consecutive channels of one token.
 
 #include "kernels.h"
 #include "stream.h"
@@ -787,27 +787,16 @@ __device__ __forceinline__ void pp_mma(const PpFrags<WT>& f, int j, PpAcc<WT>& a
   using P = PpTypes<WT>;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if constexpr (sizeof(WT) == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int t = 0; t < P::kW; ++t) {
+      bf16x8 w;
+      if constexpr (sizeof(WT) == 2)
+        w = __builtin_bit_cast(bf16x8, f.w[t][h]);
+      else
+        w = as_frag(e4m3x8_to_frag_bits(f.w[t][0][2 * h], f.w[t][0][2 * h + 1]));
 #pragma unroll
-        for (int t = 0; t < P::kW; ++t)
-#pragma unroll
-          for (int u = 0; u < P::kX; ++u)
-            acc[t][u] = mfma16x16x4f32(__uint_as_float(f.w[t][h][i]),
-                                       __uint_as_float(f.x[j][u][h][i]), acc[t][u]);
-    } else {
-#pragma unroll
-      for (int t = 0; t < P::kW; ++t) {
-        bf16x8 w;
-        if constexpr (sizeof(WT) == 2)
-          w = __builtin_bit_cast(bf16x8, f.w[t][h]);
-        else
-          w = as_frag(e4m3x8_to_frag_bits(f.w[t][0][2 * h], f.w[t][0][2 * h + 1]));
-#pragma unroll
-        for (int u = 0; u < P::kX; ++u)
-          acc[t][u] = mfma16x16x32(w, __builtin_bit_cast(bf16x8, f.x[j][u][h]), acc[t][u]);
-      }
+      for (int u = 0; u < P::kX; ++u)
+        acc[t][u] = mfma16x16x32(w, __builtin_bit_cast(bf16x8, f.x[j][u][h]), acc[t][u]);
     }
   }
 }
@@ -1160,19 +1149,31 @@ __global__ __launch_bounds__(kReduceThreads) void linear_reduce_kernel(LinearArg
   LinQuad<AT, kGated> quad;
   quad.init(a, static_cast<int>(o % quads) * 4);
   f32x4 zg[1] = {f32x4{0.f, 0.f, 0.f, 0.f}}, zu[1] = {zg[0]};
-  for (int z = 0; z < a.splits; ++z) {
-    const float* p = a.part + (static_cast<size_t>(z) * a.M + m) * a.R + quad.n;
-    if (a.N % 4 == 0) {
-      zg[0] += *reinterpret_cast<const f32x4*>(p);
-      if (kGated) zu[0] += *reinterpret_cast<const f32x4*>(p + a.N);
-    } else {
+  // four ranges' loads at a time (ranges past the last repeat it, not added)
+  for (int z0 = 0; z0 < a.splits; z0 += 4) {
+    f32x4 g[4], u[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (v < quad.valid) {
-          zg[0][v] += p[v];
-          if (kGated) zu[0][v] += p[a.N + v];
+    for (int i = 0; i < 4; ++i) {
+      const int z = min(z0 + i, a.splits - 1);
+      const float* p = a.part + (static_cast<size_t>(z) * a.M + m) * a.R + quad.n;
+      if (a.N % 4 == 0) {
+        g[i] = *reinterpret_cast<const f32x4*>(p);
+        if (kGated) u[i] = *reinterpret_cast<const f32x4*>(p + a.N);
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int c = min(v, quad.valid - 1);  // (never stored past valid)
+          g[i][v] = p[c];
+          if (kGated) u[i][v] = p[a.N + c];
         }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (z0 + i < a.splits) {
+        zg[0] += g[i];
+        if (kGated) zu[0] += u[i];
+      }
   }
   quad.template values<1>(a, zg, zu);
   quad.store(a, zg[0], m);
@@ -1572,7 +1573,8 @@ static hipError_t launch_type(LinearArgs a, hipStream_t s) {
       break;
     case kTile128Pair: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 2>(a, s); break;
     case kTile128x64:
-      if constexpr (sizeof(WT) != 4) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, sizeof(WT) == 1 ? 4 : 6>(a, s);
+      if constexpr (sizeof(WT) != 4)
+        e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, sizeof(WT) == 1 ? 4 : 6>(a, s);
       break;
     case kTile128x64Pair:
       if constexpr (sizeof(WT) != 1) e = launch_tile<WT, LinGeom<WT, 4, 2, 2, 2>, 3>(a, s);
