@@ -1149,7 +1149,8 @@ __global__ __launch_bounds__(kReduceThreads) void linear_reduce_kernel(LinearArg
   LinQuad<AT, kGated> quad;
   quad.init(a, static_cast<int>(o % quads) * 4);
   f32x4 zg[1] = {f32x4{0.f, 0.f, 0.f, 0.f}}, zu[1] = {zg[0]};
-  // four ranges' loads at a time (ranges past the last repeat it, not added)
+  // four ranges' loads at a time (ranges past the last repeat it, not added; one
+  // at a time 51 x 136 x 5704 fp32 took 18.5 us, so 15.0, eight the same)
   for (int z0 = 0; z0 < a.splits; z0 += 4) {
     f32x4 g[4], u[4];
 #pragma unroll
