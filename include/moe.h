@@ -85,6 +85,8 @@ extern "C" {
 #define MOE_ERR_BAD_ARG (-9)       /* any other invalid argument            */
 #define MOE_ERR_NOALLOC_SIZE (-10) /* moe_forward_noalloc: workspace needed  */
                                    /* exceeds MOE_NOALLOC_WORKSPACE_BYTES    */
+#define MOE_ERR_OVERLAP (-11)      /* moe_linear, moe_decode: out overlaps   */
+                                   /* an input, or the workspace a buffer    */
 
 /* ---- dtypes and scale modes ---- */
 #define MOE_DTYPE_F32 0
@@ -312,7 +314,9 @@ MOE_API int moe_quantize_act(const moe_desc* desc, const void* x, uint8_t* codes
  * dtype; sums in another order, so equal within rounding), for the sizes
  * where the number of launches and the tail of each are felt: moe_forward
  * takes three to six there.  residual [T, d] (act dtype) may be NULL, or out
- * itself; otherwise out overlaps no input.
+ * itself; an out that overlaps an input in any other way (residual and out
+ * both x, say), or a workspace that overlaps another buffer, is refused with
+ * MOE_ERR_OVERLAP.
  *   - desc: block_m 0, act_quant MOE_ACT_AS_IS, T <= MOE_DECODE_MAX_TOKENS.
  *   - schedule: between the two halves of the layer each workgroup needs the
  *     others' part of h.  MOE_SCHED_AUTO waits for it, and computes a part
@@ -379,7 +383,10 @@ MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* byte
 
 /* The product above on `stream`.  `scale` is required for e4m3fn weights and
  * NULL otherwise; bias and residual may be NULL.  out may be the residual
- * itself (same address and row stride); otherwise out overlaps no input.
+ * itself (same address and row stride); an out with an element of another
+ * input, or of another row of the residual, or a workspace that overlaps a
+ * buffer, is refused with MOE_ERR_OVERLAP.  Rows that lie between each other
+ * (column slices of one wider matrix) do not overlap.
  * The elements of out's rows past N are left as they are.  `workspace`:
  * moe_linear_workspace_bytes(desc) bytes, 256-byte aligned (may be NULL when
  * that is 0), of its own for every call that may overlap another.  The result

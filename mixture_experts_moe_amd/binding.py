@@ -43,6 +43,7 @@ ENTRY_POINTS = (
     "moe_linear_workspace_bytes", "moe_linear", "moe_decode_workspace_bytes", "moe_decode",
 )
 MOE_ERR_NOALLOC_SIZE = -10
+MOE_ERR_OVERLAP = -11
 MOE_NOALLOC_WORKSPACE_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 16
 
@@ -607,7 +608,9 @@ def moe_decode(x: torch.Tensor, w_gate: torch.Tensor, w13: torch.Tensor, w2: tor
                schedule: str = "auto") -> torch.Tensor:
     """out [T, d] = residual + MoE(x) for at most MOE_DECODE_MAX_TOKENS tokens,
     in two launches (moe_forward's layer; other arguments as there).
-    residual [T, d] in x's dtype, or None; out may be the residual."""
+    residual [T, d] in x's dtype, or None.  out may be the residual, but not
+    while that is x: an out that overlaps an input in any other way raises
+    MoEError (MOE_ERR_OVERLAP)."""
     T, d, E, I = _shapes(x, w_gate, w13, w2)
     if out is not None:
         _check_out(out, x)
@@ -665,7 +668,9 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
     pairs; activation None, "relu", "silu", "gelu" or "gelu_tanh"; bias fp32
     [rows of w]; scale fp32 [rows of w] or [1], for e4m3fn weights; residual
     and out [M, N].  Rows may be longer in memory than K or N (views of wider
-    matrices).  out may be the residual."""
+    matrices).  out may be the residual (the same view of it), but not while
+    that is x: an out that shares elements with an input in any other way
+    raises MoEError (MOE_ERR_OVERLAP)."""
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [M, K] and w [rows, K]")
     if activation not in _FNS:

@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "overlap.h"
 #include "moe.h"
 
 // Workspace of moe_forward_noalloc: one array per GPU, in the code object's
@@ -93,6 +94,16 @@ int check_ptrs(std::initializer_list<const void*> ptrs) {
     if (!p) return MOE_ERR_NULL_PTR;
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+// What a call writes against what it reads: workgroups store out while others
+// still read x, the weights or another row of the residual.
+int check_overlap(const moe::Rows& out, std::initializer_list<moe::Rows> inputs,
+                  const moe::Rows& workspace) {
+  if (moe::rows_overlap(out, workspace)) return MOE_ERR_OVERLAP;
+  for (const moe::Rows& in : inputs)
+    if (moe::rows_overlap(out, in) || moe::rows_overlap(workspace, in)) return MOE_ERR_OVERLAP;
   return MOE_OK;
 }
 
@@ -494,6 +505,7 @@ MOE_API const char* moe_strerror(int status) {
     case MOE_ERR_HIP: return "a HIP call or kernel launch failed";
     case MOE_ERR_BAD_BLOCK_M: return "block_m must be 0, 16, 32, 64, 128 or 256 (256: bf16 weights, d % 256 == 0, I % 128 == 0, 4*I*d and 2*T*d under 2^31)";
     case MOE_ERR_BAD_ARG: return "invalid argument (reserved fields must be 0)";
+    case MOE_ERR_OVERLAP: return "out overlaps an input (the residual at the same address and row stride excepted) or the workspace overlaps another buffer";
     case MOE_ERR_NOALLOC_SIZE: return "the layer needs more workspace than moe_forward_noalloc's static array (MOE_NOALLOC_WORKSPACE_BYTES, 64 MiB); call moe_forward with a caller workspace";
   }
   return "unknown status";
@@ -920,11 +932,27 @@ MOE_API int moe_decode(const moe_desc* desc, const void* x, const float* w_gate,
   if (!aligned16(residual)) return MOE_ERR_MISALIGNED;
   if (!workspace || workspace_bytes < p.total) return MOE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return MOE_ERR_MISALIGNED;
+  const bool fp8 = desc->weight_dtype == MOE_DTYPE_E4M3FN;
+  {
+    const int64_t d = desc->hidden, E = desc->num_experts, I = desc->intermediate;
+    const int64_t tokens = desc->num_tokens * d * act_bytes(desc->act_dtype);
+    const int64_t esz = fp8 ? 1 : act_bytes(desc->weight_dtype);
+    const bool channel = fp8 && scales->mode == MOE_SCALE_PER_CHANNEL;
+    using moe::span_of;
+    // (out[t, n] is written by the thread that has read residual[t, n])
+    st = check_overlap(span_of(out, tokens),
+                       {span_of(x, tokens), span_of(w_gate, E * d * 4),
+                        span_of(w13, E * 2 * I * d * esz), span_of(w2, E * d * I * esz),
+                        span_of(fp8 ? scales->w13 : nullptr, fp8 ? E * (channel ? 2 * I : 1) * 4 : 0),
+                        span_of(fp8 ? scales->w2 : nullptr, fp8 ? E * (channel ? d : 1) * 4 : 0),
+                        span_of(residual, residual && residual != out ? tokens : 0)},
+                       span_of(workspace, static_cast<int64_t>(p.total)));
+    if (st) return st;
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   int cus = 0;
   if ((st = stream_cus(s, &cus))) return st;
   char* ws = static_cast<char*>(workspace);
-  const bool fp8 = desc->weight_dtype == MOE_DTYPE_E4M3FN;
   moe::DecodeArgs a{};
   a.x = x;
   a.w_gate = w_gate;
@@ -1023,11 +1051,28 @@ MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w
   if (scaled && !scale) return MOE_ERR_NULL_PTR;
   if (!scaled && scale) return MOE_ERR_BAD_DTYPE;
   if (!aligned16(scale) || !aligned16(bias) || !aligned16(residual)) return MOE_ERR_MISALIGNED;
-  if (const size_t need = moe::linear_workspace(&a, nullptr)) {
+  const size_t need = moe::linear_workspace(&a, nullptr);
+  if (need) {
     if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) return MOE_ERR_MISALIGNED;
-    moe::linear_workspace(&a, workspace);
   }
+  {
+    const int64_t xsz = act_bytes(a.act_dtype);
+    const int64_t wsz = a.w_dtype == MOE_DTYPE_E4M3FN ? 1 : act_bytes(a.w_dtype);
+    const int64_t nscale = !scaled ? 0 : a.scale_channel ? a.R : 1;
+    // (out[m, n] is written by the thread that has read residual[m, n])
+    const bool in_place = residual == out && (a.ldr == a.ldo || a.M == 1);
+    using moe::rows_of;
+    using moe::span_of;
+    st = check_overlap(rows_of(out, a.M, a.N * xsz, a.ldo * xsz),
+                       {rows_of(x, a.M, a.K * xsz, a.ldx * xsz),
+                        rows_of(w, a.R, a.K * wsz, a.ldw * wsz), span_of(scale, nscale * 4),
+                        span_of(bias, bias ? a.R * int64_t{4} : 0),
+                        rows_of(residual, residual && !in_place ? a.M : 0, a.N * xsz, a.ldr * xsz)},
+                       span_of(workspace, static_cast<int64_t>(need)));
+    if (st) return st;
+  }
+  if (need) moe::linear_workspace(&a, workspace);
   a.x = x;
   a.w = w;
   a.scale = scale;
