@@ -4,15 +4,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-namespace moe {
+#include "linear_plan.h"
 
-// Mirrors of the ABI dtype / scale codes (moe.h), for device code.
-constexpr int kDtypeF32 = 0;
-constexpr int kDtypeBF16 = 1;
-constexpr int kDtypeE4M3FN = 2;
-constexpr int kScaleNone = 0;
-constexpr int kScaleTensor = 1;
-constexpr int kScaleChannel = 2;
+namespace moe {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
@@ -219,41 +213,6 @@ int ffn2_kchunk(int d, int I, int B, int w_dtype, int act_dtype, int64_t blocks_
 
 // ------------------------------------------------------------ dense product
 
-// Mirrors of MOE_FN_* (moe.h).
-constexpr int kFnNone = 0;
-constexpr int kFnRelu = 1;
-constexpr int kFnSilu = 2;
-constexpr int kFnGelu = 3;
-constexpr int kFnGeluTanh = 4;
-
-struct LinearArgs {
-  const void* x;       // [M, K] act dtype
-  const void* w;       // [R, K] weight dtype
-  const float* scale;  // [R] or [1], or nullptr
-  const float* bias;   // [R] or nullptr
-  const void* res;     // [M, N] act dtype or nullptr
-  void* out;           // [M, N] act dtype
-  float* part;         // [splits, M, R] fp32 (workspace) when K is split, else nullptr
-  int64_t M;
-  int N, R, K;         // R = N, or 2N when gated
-  int64_t ldx, ldw, ldr, ldo;  // elements
-  int act_dtype, w_dtype, fn;
-  bool gated, scale_channel;
-  bool vec4, vec8;     // out (and residual) rows hold aligned vectors of four, eight
-  int tile;            // the kernel that runs (linear_plan)
-  int splits;          // K ranges, each ksplit long (the last may be shorter)
-  int ksplit;
-  bool pack_x, pack_w; // rows copied to the workspace first, kpack elements each
-  int kpack;
-  void* xpack;
-  void* wpack;
-};
-
-// Chooses the kernel and the K split (the other fields set, pointers not yet
-// needed).
-void linear_plan(LinearArgs* a);
-// The workspace a plan needs; sets its pointers into `ws` unless that is null.
-size_t linear_workspace(LinearArgs* a, void* ws);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 
 // ------------------------------------------------------------ few tokens
