@@ -19,9 +19,12 @@ namespace moe {
 // z / (1 + e^-u): no cancellation for large negative z, exp overflow gives a
 // quotient of zero.
 
-// With bf16 results the sigmoids use the hardware's exp2 and reciprocal
-// (within 2^-18 of the exact quotient for any |z| below 64: a thousandth of
-// the result's half step).
+// With bf16 results the sigmoids use the hardware's exp2 and reciprocal: the
+// quotient's relative error is at most |u| 2^-23 + 2^-21 of e^-u's argument as
+// given, while that and its reciprocal are normal numbers (|u| <= 87; beyond,
+// z / (1 + e^-u) is below |z| 2^-125 and may come out as zero).  gelu_tanh's u
+// grows with z^3 and carries roundings of its own, |u| 2^-21 in all: 2^-15 at
+// z = -10, where the tail ends, against the result's half step of 2^-8 at most.
 template <bool kFast>
 __device__ __forceinline__ float lin_sigmoid_times(float z, float u) {  // z / (1 + e^-u)
   if constexpr (kFast) return z * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
