@@ -66,12 +66,15 @@ constexpr int kLinStreamTokens = 16;
 // estimated time.  A workgroup's K stage takes what its loads take (a part
 // that does not depend on the size and about 60 GB/s per compute unit,
 // shared by the workgroups on it) or what its MFMAs take; workgroups run in
-// rounds of as many as a compute unit's LDS holds.  Split sums are written
-// and read once more.  The constants were fitted to the tiles' times alone
-// and side by side (one workgroup per unit: 128 x 128 0.81 us a stage, 64 x 64
-// 0.54; the 256 x 256 tile 1.08).  Of every tile with one to three K ranges
-// the choice measured within 12% of the best at 20 sizes of 64..3305 tokens x
-// 2000..28672 rows x 80..8192 K in bf16 and e4m3fn.
+// rounds of as many as a compute unit's LDS holds; the raster gives each XCD
+// whole tiles, so that with few of them some XCDs have one more than others, or
+// none (333 x 1696 x 8752 bf16, 42 tiles of 128 x 128: six K ranges 44 us, four
+// 35).  Split sums are written and read once more.  The constants were fitted to
+// the tiles' times alone and side by side (one workgroup per unit: 128 x 128 0.81
+// us a stage, 64 x 64 0.54; the 256 x 256 tile 1.08).  Against every tile with
+// every number of K ranges the choice is on average 4% slower than the best in
+// bf16 (83 sizes of 17..4096 tokens x 64..14336 rows and K; at worst 21%), 3% in
+// e4m3fn (74; 14%) and 7% in fp32 (81; 28%).
 
 enum LinearTile { kTileStream4, kTileStream16, kTileStream16Pair, kTile256, kTile128, kTile128Pair,
                   kTile128x64, kTile128x64Pair, kTile64, kTileStaged128, kTileStaged64 };
@@ -97,6 +100,7 @@ constexpr TileCost kTileCosts[] = {
     {kTileStaged64, 64, 64, 1 | 2 | 4, {16, 12}, 0.7f, 1.f},
 };
 constexpr int kComputeUnits = 256;
+constexpr int kRasterXcds = 8;
 constexpr float kUsPerKb = 0.017f;
 
 // The tile and K ranges of the least estimated time among the aligned tiles
@@ -125,7 +129,12 @@ inline float linear_choose(LinearArgs* a, bool aligned) {
       if (want > 1 && per < 4 * kc) break;
       const int splits = (a->K + per - 1) / per;
       const float stages = static_cast<float>((per + kc - 1) / kc);
-      const int64_t here = (tiles * splits + kComputeUnits - 1) / kComputeUnits;  // per unit
+      // workgroups of the compute unit that has most (the aligned tiles' raster
+      // is per XCD, the staged ones' workgroups go to the units in turn)
+      constexpr int kUnits = kComputeUnits / kRasterXcds;
+      const int64_t here =
+          aligned ? ((tiles + kRasterXcds - 1) / kRasterXcds * splits + kUnits - 1) / kUnits
+                  : (tiles * splits + kComputeUnits - 1) / kComputeUnits;
       auto round_us = [&](int n) {
         float stage = t.fixed + kUsPerKb * kb;
         if (n * kUsPerKb * kb > stage) stage = n * kUsPerKb * kb;

@@ -31,7 +31,15 @@ KERNELS = [("bf16", 65, 1440, 7360, False), ("bf16", 17, 8128, 3264, True),
            ("f32", 72, 751, 2167, True), ("f32", 5, 69, 77, False),
            ("f32", 8, 1392, 4913, True),
            ("f32", 533, 508, 199, False), ("f32", 737, 172, 193, True),
-           ("f32", 1400, 2100, 1999, False)]
+           ("f32", 1400, 2100, 1999, False), ("bf16", 2633, 80, 4688, False),
+           ("bf16", 19, 3824, 2000, True), ("bf16", 68, 5440, 2512, False),
+           ("bf16", 17, 5040, 1488, True), ("f32", 67, 8296, 688, False),
+           ("f32", 72, 9104, 2176, False), ("f32", 66, 4424, 2240, True),
+           ("f32", 17, 8304, 792, False), ("f32", 71, 8320, 880, False),
+           ("f32", 66, 4112, 864, True), ("f32", 589, 11910, 67, False),
+           ("f32", 65, 8230, 865, False), ("f32", 669, 5362, 67, True),
+           ("f32", 81, 4222, 875, True), ("f32", 1700, 2301, 2501, True),
+           ("f32", 1500, 3796, 2842, False)]
 
 
 @pytest.mark.parametrize("fmt,M,N,K,gated", KERNELS)
