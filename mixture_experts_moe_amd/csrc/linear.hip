@@ -268,7 +268,8 @@ struct LinOct {
     }
     AT* o = static_cast<AT*>(a.out) + m * a.ldo + n;
     const AT* r = static_cast<const AT*>(a.res) + m * a.ldr + n;
-    if (a.vec8 && valid == 8) {
+    // (two 16-byte pieces of four fp32, or one of eight bf16)
+    if ((sizeof(AT) == 4 ? a.vec4 : a.vec8) && valid == 8) {
       constexpr int kParts = sizeof(AT) == 4 ? 2 : 1;  // 16-byte pieces
 #pragma unroll
       for (int p = 0; p < kParts; ++p) {

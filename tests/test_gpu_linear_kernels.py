@@ -5,7 +5,7 @@ two lists against the library's choice; tolerance as there)."""
 import pytest
 
 from mixture_experts_moe_amd import binding as B
-from test_gpu_linear import FNS, check, inputs
+from test_gpu_linear import FNS, check, inputs, padded
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,19 @@ def test_values(M, N, K, gated, fmt):
     x, w, b, scale, r = inputs(M, N, K, fmt, gated, bias=(N + K) % 3 > 0, residual=M % 2 > 0)
     out = B.moe_linear(x, w, bias=b, activation=fn, gated=gated, scale=scale, residual=r)
     check(out, x, w, fn, gated, b, scale, r)
+
+
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "e4m3fn"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("opad,rpad", [(0, 0), (4, 0), (0, 4), (4, 8), (2, 0), (8, 2)])
+@pytest.mark.parametrize("M,N,K", [(7, 52, 64), (40, 100, 128), (300, 260, 1024), (1500, 1300, 128)])
+def test_rows_of_every_alignment_leave_whole(M, N, K, opad, rpad, gated, fmt):
+    """Vectors of eight, of four and single elements of out and the residual;
+    what lies between out's rows stays."""
+    print(f"linear rows {M}x{N}x{K} +{opad} +{rpad} gated={gated} {fmt}", flush=True)
+    x, w, b, scale, r = inputs(M, N, K, fmt, gated)
+    _, rv = padded(r, rpad, float("nan"))
+    buf, out = padded(r, opad, 7.0)
+    B.moe_linear(x, w, bias=b, activation="relu", gated=gated, scale=scale, residual=rv, out=out)
+    check(out, x, w, "relu", gated, b, scale, r)
+    assert (buf[:, N:] == 7.0).all()
