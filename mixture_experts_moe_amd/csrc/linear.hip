@@ -1425,7 +1425,7 @@ static hipError_t launch_type(LinearArgs a, hipStream_t s) {
     // a ring of four stages alone on its compute unit, or less LDS and two
     // workgroups side by side
     case kTile128:
-      if constexpr (sizeof(WT) != 1) e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 4>(a, s);
+      if constexpr (sizeof(WT) == 2) e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 4>(a, s);
       break;
     case kTile128Pair: e = launch_tile<WT, LinGeom<WT, 2, 4, 4, 2>, 2>(a, s); break;
     case kTile128x64:

@@ -65,16 +65,18 @@ constexpr int kLinStreamTokens = 16;
 // More than 16 tokens: the tile and the number of K ranges with the least
 // estimated time.  A workgroup's K stage takes what its loads take (a part
 // that does not depend on the size and about 60 GB/s per compute unit,
-// shared by the workgroups on it) or what its MFMAs take; workgroups run in
-// rounds of as many as a compute unit's LDS holds; the raster gives each XCD
-// whole tiles, so that with few of them some XCDs have one more than others, or
-// none (333 x 1696 x 8752 bf16, 42 tiles of 128 x 128: six K ranges 44 us, four
-// 35).  Split sums are written and read once more.  The constants were fitted to
-// the tiles' times alone and side by side (one workgroup per unit: 128 x 128 0.81
-// us a stage, 64 x 64 0.54; the 256 x 256 tile 1.08).  Against every tile with
-// every number of K ranges the choice is on average 4% slower than the best in
-// bf16 (83 sizes of 17..4096 tokens x 64..14336 rows and K; at worst 21%), 3% in
-// e4m3fn (74; 14%) and 7% in fp32 (81; 28%).
+// shared by the workgroups on it) or what its MFMAs take; in fp32 the MFMAs are
+// nearly all of a stage and it takes a multiple of theirs that was measured for
+// each tile.  Workgroups run in rounds of as many as a compute unit's LDS holds;
+// the raster gives each XCD whole tiles, so that with few of them some XCDs have
+// one more than others, or none (333 x 1696 x 8752 bf16, 42 tiles of 128 x 128:
+// six K ranges 44 us, four 35).  Split sums are written and read once more.
+// The constants were fitted to the tiles' times alone and side by side (bf16,
+// one workgroup per unit: 128 x 128 0.81 us a stage, 64 x 64 0.54; the 256 x 256
+// tile 1.08).  Against every tile with every number of K ranges the choice is
+// on average 4% slower than the best in bf16 (83 sizes of 17..4096 tokens x
+// 64..14336 rows and K; at worst 21%), 3% in e4m3fn (74; 14%) and 2% in fp32
+// (141; 16%).
 
 enum LinearTile { kTileStream4, kTileStream16, kTileStream16Pair, kTile256, kTile128, kTile128Pair,
                   kTile128x64, kTile128x64Pair, kTile64, kTileStaged128, kTileStaged64 };
@@ -85,19 +87,22 @@ struct TileCost {
   int lds_kb[2];  // stages in LDS: with weights of two or four bytes, of one
   float fixed;    // us per stage apart from the bytes
   float start;    // us per workgroup: first loads and epilogue
+  // fp32: a stage in times of its MFMAs, of one workgroup and of each of several
+  // on a compute unit, and `start`
+  float alone, shared, start32;
 };
 // the aligned tiles, then the staged ones (a tile is not built for types whose
 // every size has a cheaper one: fp32 is bound by its MFMAs in any tile, and
 // e4m3fn's stages are small enough to hold two workgroups or four stages)
 constexpr TileCost kTileCosts[] = {
-    {kTile256, 256, 256, 1 | 2, {160, 128}, 0.27f, 11.f},
-    {kTile128, 128, 128, 2 | 4, {128, 96}, 0.27f, 1.f},
-    {kTile128Pair, 128, 128, 1 | 2 | 4, {64, 48}, 0.27f, 1.f},
-    {kTile128x64, 128, 64, 1 | 2, {144, 64}, 0.27f, 1.f},
-    {kTile128x64Pair, 128, 64, 2 | 4, {72, 48}, 0.27f, 1.f},
-    {kTile64, 64, 64, 1 | 2 | 4, {64, 48}, 0.25f, 0.5f},
-    {kTileStaged128, 128, 128, 1 | 2 | 4, {32, 24}, 1.2f, 1.f},
-    {kTileStaged64, 64, 64, 1 | 2 | 4, {16, 12}, 0.7f, 1.f},
+    {kTile256, 256, 256, 1 | 2, {160, 128}, 0.27f, 11.f, 0.f, 0.f, 0.f},
+    {kTile128, 128, 128, 2, {128, 96}, 0.27f, 1.f, 0.f, 0.f, 0.f},
+    {kTile128Pair, 128, 128, 1 | 2 | 4, {64, 48}, 0.27f, 1.f, 1.2f, 0.97f, 1.7f},
+    {kTile128x64, 128, 64, 1 | 2, {144, 64}, 0.27f, 1.f, 0.f, 0.f, 0.f},
+    {kTile128x64Pair, 128, 64, 2 | 4, {72, 48}, 0.27f, 1.f, 1.2f, 1.01f, 0.1f},
+    {kTile64, 64, 64, 1 | 2 | 4, {64, 48}, 0.25f, 0.5f, 1.4f, 1.16f, 0.f},
+    {kTileStaged128, 128, 128, 1 | 2 | 4, {32, 24}, 1.2f, 1.f, 1.2f, 1.04f, 5.5f},
+    {kTileStaged64, 64, 64, 1 | 2 | 4, {16, 12}, 0.7f, 1.f, 1.48f, 1.25f, 0.f},
 };
 constexpr int kComputeUnits = 256;
 constexpr int kRasterXcds = 8;
@@ -116,10 +121,7 @@ inline float linear_choose(LinearArgs* a, bool aligned) {
     const int64_t tiles = ((a->M + t.tokens - 1) / t.tokens) * ((a->R + t.rows - 1) / t.rows);
     const float kb = (t.rows * kc * wb + t.tokens * 128) / 1024.f;
     // a compute unit's MFMAs: 4096 flops a clock in bf16, 256 in fp32, 2.1 GHz
-    // (fp32's are all of a stage and leave gaps between stages; staged tiles
-    // overlap them with little else)
-    const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f *
-                       (!aligned ? 1.6f : wb == 4 ? 1.35f : 1.1f);
+    const float mfma = 2.f * t.rows * t.tokens * kc / (wb == 4 ? 256.f : 4096.f) / 2100.f;
     const int waves = t.rows == 64 ? 4 : 8;
     int held = 160 / t.lds_kb[wb == 1];
     if (held > 16 / waves) held = 16 / waves;
@@ -136,15 +138,19 @@ inline float linear_choose(LinearArgs* a, bool aligned) {
           aligned ? ((tiles + kRasterXcds - 1) / kRasterXcds * splits + kUnits - 1) / kUnits
                   : (tiles * splits + kComputeUnits - 1) / kComputeUnits;
       auto round_us = [&](int n) {
+        if (wb == 4) return stages * mfma * (n == 1 ? t.alone : n * t.shared) + t.start32;
+        // (staged tiles overlap their MFMAs with little else)
+        const float products = n * mfma * (aligned ? 1.1f : 1.6f);
         float stage = t.fixed + kUsPerKb * kb;
         if (n * kUsPerKb * kb > stage) stage = n * kUsPerKb * kb;
-        if (n * mfma > stage) stage = n * mfma;
+        if (products > stage) stage = products;
         return stages * stage + t.start;
       };
       float us = (here / held) * round_us(held);
       if (here % held) us += round_us(static_cast<int>(here % held));
       if (us < bytes / 4.7e6f) us = bytes / 4.7e6f;
-      if (splits > 1) us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / 3e6f;
+      if (splits > 1)
+        us += 2.5f + static_cast<float>(splits) * a->M * a->R * 8.f / (wb == 4 ? 5e6f : 3e6f);
       if (us < best) {
         best = us;
         a->tile = t.tile;

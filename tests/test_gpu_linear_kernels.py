@@ -39,7 +39,9 @@ KERNELS = [("bf16", 65, 1440, 7360, False), ("bf16", 17, 8128, 3264, True),
            ("f32", 66, 4112, 864, True), ("f32", 589, 11910, 67, False),
            ("f32", 65, 8230, 865, False), ("f32", 669, 5362, 67, True),
            ("f32", 81, 4222, 875, True), ("f32", 1700, 2301, 2501, True),
-           ("f32", 1500, 3796, 2842, False)]
+           ("f32", 1500, 3796, 2842, False), ("f32", 457, 12368, 280, False),
+           ("f32", 200, 13312, 288, True), ("f32", 649, 10455, 215, False),
+           ("f32", 66, 3264, 4863, False), ("f32", 68, 4468, 1677, True)]
 
 
 @pytest.mark.parametrize("fmt,M,N,K,gated", KERNELS)
