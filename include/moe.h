@@ -378,7 +378,8 @@ typedef struct moe_linear_desc {
 
 /* Bytes of device workspace moe_linear needs for `desc`: 0 unless K is split
  * over workgroups (few tiles) or rows that are not multiples of 16 bytes apart
- * are worth copying first (more than four tokens). */
+ * are worth copying first (x: more than four tokens; W: more than 16, and then
+ * all of it on every call). */
 MOE_API int moe_linear_workspace_bytes(const moe_linear_desc* desc, size_t* bytes);
 
 /* The product above on `stream`.  `scale` is required for e4m3fn weights and

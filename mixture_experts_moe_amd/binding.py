@@ -668,7 +668,8 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
     pairs; activation None, "relu", "silu", "gelu" or "gelu_tanh"; bias fp32
     [rows of w]; scale fp32 [rows of w] or [1], for e4m3fn weights; residual
     and out [M, N].  Rows may be longer in memory than K or N (views of wider
-    matrices).  out may be the residual (the same view of it), but not while
+    matrices) and of any length; every tensor starts at a multiple of 16 bytes
+    (a slice that does not raises MoEError, MOE_ERR_MISALIGNED).  out may be the residual (the same view of it), but not while
     that is x: an out that shares elements with an input in any other way
     raises MoEError (MOE_ERR_OVERLAP)."""
     if x.dim() != 2 or w.dim() != 2:

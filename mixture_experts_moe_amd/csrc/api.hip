@@ -497,11 +497,11 @@ MOE_API const char* moe_strerror(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_NULL_PTR: return "a required pointer is NULL";
-    case MOE_ERR_BAD_SHAPE: return "bad shape (d and I must be multiples of 64 in [64, 2^19], 1 <= E <= 1024, T >= 0, T*top_k < 2^30)";
+    case MOE_ERR_BAD_SHAPE: return "bad shape (d and I must be multiples of 64 in [64, 2^19], 1 <= E <= 1024, T >= 0, T*top_k < 2^30; moe_decode: T <= 16; moe_linear: 0 <= M <= 2^28, 1 <= N, K <= 2^20, M*N <= 2^34, row strides 0 or from the row's length to 2^20)";
     case MOE_ERR_BAD_TOPK: return "top_k must be in [1, min(E, 64)]";
     case MOE_ERR_BAD_DTYPE: return "unsupported dtype pair or scale mode (supported: f32/f32, bf16/bf16, bf16/e4m3fn with per-tensor or per-channel scales)";
     case MOE_ERR_MISALIGNED: return "a pointer is not 16-byte aligned (workspace: 256-byte)";
-    case MOE_ERR_WORKSPACE: return "workspace is NULL or smaller than moe_workspace_bytes()";
+    case MOE_ERR_WORKSPACE: return "workspace is NULL or smaller than moe_workspace_bytes() (moe_decode_workspace_bytes(), moe_linear_workspace_bytes()) asks for";
     case MOE_ERR_HIP: return "a HIP call or kernel launch failed";
     case MOE_ERR_BAD_BLOCK_M: return "block_m must be 0, 16, 32, 64, 128 or 256 (256: bf16 weights, d % 256 == 0, I % 128 == 0, 4*I*d and 2*T*d under 2^31)";
     case MOE_ERR_BAD_ARG: return "invalid argument (reserved fields must be 0)";

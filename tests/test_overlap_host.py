@@ -172,3 +172,13 @@ def test_rows_overlap_against_sets_of_bytes(tmp_path):
     assert len(got) == len(want) and 0.2 < sum(want) / len(want) < 0.8
     wrong = [c for c, g, w in zip(cases, got, want) if g != w]
     assert not wrong, wrong[:3]
+
+
+def test_the_texts_of_refused_shapes_name_these_calls(lib):
+    """17 tokens and no output features are refused with a text that says why."""
+    d = B.make_desc(17, 128, 8, 128, BF16, BF16)
+    n = ctypes.c_size_t()
+    assert lib.moe_decode_workspace_bytes(ctypes.byref(d), 2, ctypes.byref(n)) == -2
+    assert lib.moe_linear_workspace_bytes(ctypes.byref(desc(N=0)), ctypes.byref(n)) == -2
+    assert "moe_decode: T <= 16" in B.strerror(-2) and "moe_linear: 0 <= M" in B.strerror(-2)
+    assert "moe_linear_workspace_bytes" in B.strerror(-6)
