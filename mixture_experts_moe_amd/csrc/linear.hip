@@ -968,8 +968,9 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinearArgs a, 
 // S stages in LDS arrays of their own (reads of one stage then wait for no
 // load into another): S - 1 stages are in flight while one is multiplied, so
 // a workgroup alone on its compute unit covers the memory latency.  What is
-// left is what a compute unit takes in, about 60 GB/s of 128-byte row pieces:
-// 0.42 us for a 64 x 64 stage, alike with four stages and with eight.
+// left is a fixed part of every stage (barrier, waits, fragment reads: 0.25 us)
+// and what a compute unit takes in, about 60 GB/s of 128-byte row pieces: 0.54 us
+// for the 16 KB of a 64 x 64 stage, alike with four stages and with eight.
 
 // One operand of a tile: kRows rows, of which [0, kSplit) start at one base
 // and the rest at another (gated weights; else kSplit = kRows).
