@@ -669,9 +669,10 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor]
     [rows of w]; scale fp32 [rows of w] or [1], for e4m3fn weights; residual
     and out [M, N].  Rows may be longer in memory than K or N (views of wider
     matrices) and of any length; every tensor starts at a multiple of 16 bytes
-    (a slice that does not raises MoEError, MOE_ERR_MISALIGNED).  out may be the residual (the same view of it), but not while
-    that is x: an out that shares elements with an input in any other way
-    raises MoEError (MOE_ERR_OVERLAP)."""
+    (a slice that does not raises MoEError, MOE_ERR_MISALIGNED).  out may be
+    the residual (the same view of it), but not while that is x: an out that
+    shares elements with an input in any other way raises MoEError
+    (MOE_ERR_OVERLAP)."""
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [M, K] and w [rows, K]")
     if activation not in _FNS:
