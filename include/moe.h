@@ -425,7 +425,9 @@ MOE_API int moe_linear(const moe_linear_desc* desc, const void* x, const void* w
  * scale NaN and codes 0; scales are at least 2^-126.  A code is the nearest
  * one but for values within 2^-16 of a step of the middle between two.  Squares
  * are summed in fp32: a row is normalised right while that sum is finite (|h|
- * up to about 1e19 / sqrt(cols)).
+ * up to about 1e19 / sqrt(cols)) and mean(h^2) + eps at least 2^-126; below, with
+ * an eps that does not hold it there, the squares lose their last bits (|h| about
+ * 1e-20: a relative error of 1e-5) and from about 1e-22 down vanish.
  * Limits: 0 <= rows < 2^31, 1 <= cols <= 2^20, row strides at most 2^20, eps
  * >= 0 and finite.  One launch; capturable into a graph; not timed
  * (moe_timing_enable). */
@@ -456,9 +458,9 @@ MOE_API int moe_rmsnorm(const moe_norm_desc* desc, const void* x, const void* re
  * themselves (same address and row stride; its stride is desc->ldx).  Rows up
  * to 16 KiB are read once, longer ones twice.  `workspace`: 256-byte aligned,
  * moe_rmsnorm_backward_workspace_bytes(desc) bytes (may be NULL when that is
- * 0), of its own for every call that may overlap another.  dweight's sums have
- * a fixed order.  rows = 0 leaves dweight as it is.  Limits and the rest as
- * moe_rmsnorm. */
+ * 0), of its own for every call that may overlap another, with a dweight or
+ * without.  dweight's sums have a fixed order.  rows = 0 leaves dweight as it is.
+ * Limits and the rest as moe_rmsnorm; mean(g h), too, is summed in fp32. */
 MOE_API int moe_rmsnorm_backward_workspace_bytes(const moe_norm_desc* desc, size_t* bytes);
 MOE_API int moe_rmsnorm_backward(const moe_norm_desc* desc, const void* dy, const void* h,
                                  const float* weight, const void* dsum, void* dx, float* dweight,

@@ -385,6 +385,8 @@ __global__ __launch_bounds__(kNormLong) void norm_long_kernel(NormArgs a) {
 //
 // With g = w dy:  dh = (g - h r^2 mean(g h)) r (+ dsum),  dw = sum of dy h r.
 // r and mean(g h) come from the rows themselves, which have to be read anyway.
+// The second term is (h r)(r mean(g h)): |h r| is at most sqrt(cols), while r^2
+// leaves fp32 where mean(h^2) + eps is below 3e-39 and dh is far from its limits.
 // A workgroup walks every gridDim.x-th row with its columns' share of dw in
 // registers; the workgroups' shares are added by a second launch, in order, so
 // dw does not depend on the run.  The next row is loaded while one is worked on.
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(NormGeom<kLanes>::kThreads, 4) void norm_backward_k
     }
     norm_over_row2<kLanes>(hh, gh, red);
     const float r = 1.0f / sqrtf(hh / a.cols + a.eps);
-    const float c = r * r * (gh / a.cols);
+    const float k = r * (gh / a.cols);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       float h[N], g[N], s[N];
@@ -469,8 +471,9 @@ __global__ __launch_bounds__(NormGeom<kLanes>::kThreads, 4) void norm_backward_k
       if (a.dsum) R::values(qs[u], s);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        dw[u][i] += g[i] * (h[i] * r);
-        s[i] += (g[i] * w[u][i] - h[i] * c) * r;
+        const float n = h[i] * r;
+        dw[u][i] += g[i] * n;
+        s[i] += (g[i] * w[u][i] - n * k) * r;
       }
       R::store(static_cast<AT*>(a.dx) + m * a.ldx, (u * kLanes + lane) * N, a.cols, R::rounded(s));
     }
@@ -495,7 +498,7 @@ __global__ __launch_bounds__(NormGeom<kLanes>::kThreads, 4) void norm_backward_k
   }
 }
 
-// Rows that registers do not hold: r and r^2 mean(g h) of every row first ...
+// Rows that registers do not hold: r and r mean(g h) of every row first ...
 template <typename AT>
 __global__ __launch_bounds__(kNormLong) void norm_backward_stats_kernel(NormBackwardArgs a) {
   using R = NormRow<AT>;
@@ -519,7 +522,7 @@ __global__ __launch_bounds__(kNormLong) void norm_backward_stats_kernel(NormBack
   const float r = 1.0f / sqrtf(hh / a.cols + a.eps);
   if (threadIdx.x == 0) {
     a.stats[2 * m] = r;
-    a.stats[2 * m + 1] = r * r * (gh / a.cols);
+    a.stats[2 * m + 1] = r * (gh / a.cols);
   }
 }
 // ... then a workgroup takes 256 units of columns (blockIdx.y) of every
@@ -545,8 +548,9 @@ __global__ __launch_bounds__(kNormCols) void norm_backward_long_kernel(NormBackw
     if (a.dsum) R::values(R::raw(static_cast<const AT*>(a.dsum) + m * a.ldsum, c, a.cols), s);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      dw[i] += g[i] * (h[i] * r);
-      s[i] += (g[i] * w[i] - h[i] * k) * r;
+      const float n = h[i] * r;
+      dw[i] += g[i] * n;
+      s[i] += (g[i] * w[i] - n * k) * r;
     }
     R::store(static_cast<AT*>(a.dx) + m * a.ldx, c, a.cols, R::rounded(s));
   }
