@@ -771,7 +771,7 @@ class RmsNorm(NamedTuple):
     """What moe_rmsnorm returns; None for what was not asked for."""
 
     y: Optional[torch.Tensor]
-    sum: torch.Tensor                   # x + residual, or x
+    sum: Optional[torch.Tensor]         # x + residual, or x unless y replaced it
     codes: Optional[torch.Tensor]
     scale: Optional[torch.Tensor]
 
@@ -836,8 +836,9 @@ def moe_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e
     float32 scale [T] instead (y = codes * scale, scale = max |y| / 127); or
     "both".  Returns RmsNorm(y, sum, codes, scale); sum is h, rounded to x's
     dtype before it is normalised.  sum_out and out take sum and y; each may be
-    x or residual itself (the same view of it), which updates it in place.  Rows
-    may be longer in memory than d; tensors start at multiples of 16 bytes."""
+    x or residual itself (the same view of it), which updates it in place; without a
+    residual an out that is x leaves no h, and sum is None.  Rows may be longer in
+    memory than d; tensors start at multiples of 16 bytes."""
     if x.dim() != 2:
         raise ValueError(f"x must be [T, d], got {list(x.shape)}")
     if outputs not in _NORM_OUTPUTS:
@@ -868,7 +869,9 @@ def moe_rmsnorm(x: torch.Tensor, weight: Optional[torch.Tensor], eps: float = 1e
         _check("moe_rmsnorm", lib().moe_rmsnorm(
             ctypes.byref(desc), x.data_ptr(), _addr(residual), _addr(weight), _addr(h), _addr(y),
             _addr(codes), _addr(scale), s))
-    return RmsNorm(y, x if h is None else h, codes, scale)
+    if h is None and (out is None or T == 0 or out.data_ptr() != x.data_ptr()):
+        h = x
+    return RmsNorm(y, h, codes, scale)
 
 
 def moe_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor],
