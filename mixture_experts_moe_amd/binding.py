@@ -967,7 +967,7 @@ def moe_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sca
     if grouped:
         if w.is_contiguous():
             ldw = 0
-        elif w.stride(2) != 1 and K > 1 or E > 1 and w.stride(0) != R * w.stride(1):
+        elif w.stride(2) != 1 and K > 1 or E > 1 and R > 1 and w.stride(0) != R * w.stride(1):
             raise ValueError(f"w must have dense rows and experts, got strides {w.stride()}")
         else:
             ldw = w.stride(1) if R > 1 else K if E <= 1 else w.stride(0)

@@ -31,3 +31,19 @@ def test_a_norm_over_its_input_returns_no_sum(outputs):
     z = x.clone()
     got = B.moe_rmsnorm(z, w, residual=res, outputs=outputs, out=z)
     assert torch.equal(got.sum, h) and torch.equal(got.y, B.moe_rmsnorm(h, w).y)
+
+
+@pytest.mark.parametrize("K", [1, 64, 200])
+def test_experts_of_one_weight_row(K):
+    """w [E, 1, K], the first rows of wider experts: rows that lie an expert apart."""
+    E, rows = 4, 5
+    g = torch.Generator(device="cuda").manual_seed(4)
+    wide = torch.randint(-128, 128, (E, rows, K), generator=g, device="cuda").to(torch.int8)
+    w = wide[:, :1]
+    x = torch.randint(-128, 128, (40, K), generator=g, device="cuda").to(torch.int8)
+    at = torch.tensor([0, 7, 7, 30, 40], dtype=torch.int32, device="cuda")
+    one, ones = torch.ones(E, device="cuda"), torch.ones(40, device="cuda")
+    out = B.moe_linear_i8(x, ones, w, one, offsets=at, out_dtype=torch.float32)
+    for e in range(E):
+        s = slice(int(at[e]), int(at[e + 1]))
+        assert torch.equal(out[s].double(), x[s].double() @ w[e].double().t()), e
