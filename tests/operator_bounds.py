@@ -123,3 +123,33 @@ def outside(got, want):
     """The share of elements that are further from the value than its bound."""
     value, tol = want
     return float((~((got.double() - value).abs() <= tol)).double().mean())
+
+
+def slopes(norm, backward, x, res, w, dy, ds, v, q, step, eps=1e-6):
+    """{name: (difference, bound)}: the slope of f = <dy, y> + <ds, sum> between norm's own results
+    on both sides of x along v (and of w along q), less the one that backward's dx (dweight) has.
+
+    Both are taken along what the rounded points really differ by.  What they may be apart by: the
+    curvature that 64 bits have between the same points, to the digit (w: f is linear, none), the
+    errors of the two y, and those of dx (dweight)."""
+    d = x.shape[1]
+    mid = norm(x, w, res)[1]
+    dx, dw = backward(dy, mid, w, ds)
+    exact = norm_gradient(dy, mid, w, eps, ds, x.dtype)
+
+    def ends(xx, ww):
+        y, h = norm(xx, ww, res)
+        y64 = norm64(h, ww, eps)[0]
+        f = [(dy.double() * t.double()).sum() + (ds.double() * h.double()).sum() for t in (y, y64)]
+        return h.double(), ww.double(), f, (e_norm(d) + U) * (dy.double() * y64).abs().sum()
+
+    def apart(a, b, got, exact, along):
+        (_, _, fa, na), (_, _, fb, nb) = a, b
+        move = along(a) - along(b)
+        curve = (fa[1] - fb[1]) - (exact[0] * move).sum()
+        diff = (fa[0] - fb[0]) - (got.double() * move).sum() - curve
+        return float(diff / (2 * step)), float((na + nb + (exact[1] * move.abs()).sum()) / (2 * step))
+
+    return {"dx": apart(ends(x + step * v, w), ends(x - step * v, w), dx, exact["dx"], lambda t: t[0]),
+            "dweight": apart(ends(x, w + step * q), ends(x, w - step * q), dw, exact["dweight"],
+                             lambda t: t[1])}

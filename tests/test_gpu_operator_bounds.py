@@ -73,3 +73,25 @@ def test_the_layer_from_its_parts(T):
     want = ob.layer(x, ids, gates, w13, w2)
     assert ob.outside(B.moe_unpermute(y, p.slot_row, weights=gates), want) == 0
     assert ob.outside(B.moe_forward(x, gate, w13, w2, k), want) == 0
+
+
+@pytest.mark.parametrize("T,d", [(3, 50), (4, 1500), (2, 5000)])
+def test_backward_against_differences(T, d):
+    """The slope between the norm's own results on both sides of x, and of the weight.  dy leans
+    towards the norm's result and v towards x, so that the gradient's second term counts."""
+    g = gen(T * d)
+    x, res, ds = (randn(g, T, d) for _ in range(3))
+    w, q = rand(g, d) + 0.5, randn(g, d)
+    dy = randn(g, T, d) + (x + res) * 0.5
+
+    def norm(xx, ww, rr):
+        n = B.moe_rmsnorm(xx, ww, EPS, residual=rr)
+        return n.y, n.sum
+
+    def backward(dy, h, w, dsum):
+        return B.moe_rmsnorm_backward(dy, h, w, EPS, dsum=dsum)
+
+    got = ob.slopes(norm, backward, x, res, w, dy, ds, randn(g, T, d) + x + res,
+                    q + (dy * (x + res)).mean(0), 2.0 ** -5)
+    for name, (diff, bound) in got.items():
+        assert abs(diff) <= bound, (name, diff, bound)

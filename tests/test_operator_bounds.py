@@ -134,3 +134,25 @@ def test_layer(plant):
     inputs = layer_inputs(60, 256, 128, 8, 2, 7)
     share = ob.outside(plain_layer(*inputs, plant), ob.layer(*inputs))
     assert share > 0 if plant else share == 0, share
+
+
+# ------------------------------------------------------------ slopes
+
+def slope_inputs(T, d, seed):
+    """dy leans towards the norm's result and v towards x, so that the gradient's second term is
+    as large as its first."""
+    g = gen(seed)
+    x, res, ds = (randn(g, T, d) for _ in range(3))
+    w, q = torch.rand(d, generator=g) + 0.5, randn(g, d)
+    dy = randn(g, T, d) + (x + res) * 0.5
+    return x, res, w, dy, ds, randn(g, T, d) + x + res, q + (dy * (x + res)).mean(0)
+
+
+@pytest.mark.parametrize("plant", [None, "second term", "dsum", "no dx", "weight", "r", "no dweight"])
+@pytest.mark.parametrize("T,d", [(3, 50), (4, 1500)])
+def test_slopes(T, d, plant):
+    x, res, w, dy, ds, v, q = slope_inputs(T, d, T)
+    got = ob.slopes(norm, lambda *a: backward(*a, plant), x, res, w, dy, ds, v, q, 2.0 ** -5)
+    hit = {None: None, "r": "dweight", "no dweight": "dweight"}.get(plant, "dx")
+    for name, (diff, bound) in got.items():
+        assert (abs(diff) > 4 * bound) if name == hit else (abs(diff) <= bound), (name, diff, bound)
