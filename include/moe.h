@@ -536,9 +536,10 @@ MOE_API int moe_linear_i8(const moe_linear_i8_desc* desc, const int8_t* x, const
  * rows_scale (both or neither) go with I8 rows.  hidden, and ldx and ldr (in
  * elements, 0 = dense), are arbitrary; buffers start at multiples of 16 bytes.
  * `workspace`: moe_permute_workspace_bytes(desc) bytes, 256-byte aligned (NULL
- * when 0).  num_rows is not looked at.  T = 0 writes nothing, offsets included.
- * Limits: T * top_k < 2^30, 1 <= top_k <= 64 (not held to num_experts), 1 <=
- * num_experts <= 1024, 1 <= hidden <= 2^20, row strides at most 2^20. */
+ * when 0), of its own for every call that may overlap another.  num_rows is not
+ * looked at.  T = 0 writes nothing, offsets included.  Limits: T * top_k < 2^30,
+ * 1 <= top_k <= 64 (not held to num_experts), 1 <= num_experts <= 1024, 1 <= hidden
+ * <= 2^20, row strides at most 2^20. */
 typedef struct moe_permute_desc {
   int64_t num_tokens;    /* T                                */
   int64_t hidden;

@@ -7,7 +7,9 @@ stream of the tensors' device).  Tensors the binding allocates (outputs,
 workspace) are allocated on that stream, so torch's caching allocator only
 reuses their memory for work ordered after these kernels.  All computation happens in
 the HIP kernels of ``libmoe.so``; there is no fallback of any kind, and if
-the library is missing the first call raises.
+the library is missing the first call raises.  No call is recorded by torch's
+autograd: results never require a gradient, whatever the inputs do, and the
+gradients that there are (``*_backward``) are calls of their own.
 """
 
 from __future__ import annotations

@@ -1410,7 +1410,7 @@ __global__ __launch_bounds__(kReduceThreads) void linear_reduce_kernel(LinearArg
 
 // ------------------------------------------------------------ few tokens
 //
-// At most 16 tokens: the product is a read of W (stream.h).  A workgroup
+// At most 16 tokens (int8: 64): the product is a read of W (stream.h).  A workgroup
 // takes 16 * RT weight rows (gated: half of them gate rows, half the matching
 // up rows), its eight waves every eighth K chunk each, so that together they
 // read 2 KB of a row at a time; the waves' sums meet in LDS in a fixed order.
@@ -1420,9 +1420,10 @@ __global__ __launch_bounds__(kReduceThreads) void linear_reduce_kernel(LinearArg
 // streaming beside one that adds (16 x 14336 gated x 4096 27.1 us with eight, 23.3
 // with four, 23.5 with two; 16 x 4096 x 14336 13.3, 13.2, 14.8).
 //
-// 17 to 64 tokens: what bounds them is what a compute unit takes in, about 45
-// GB/s, and two thirds of that or more are tokens, which pass through LDS with
-// the weights; 144 KB of it hold six waves (32 x 4096 x 14336: four 17.5 us, six
+// 17 to 64 tokens: a workgroup alone on its compute unit takes in about 45 GB/s
+// with these loads in flight (a measured rate of this kernel, no limit of the chip),
+// and two thirds of that or more are tokens, which pass through LDS with the weights;
+// 144 KB of it hold six waves (32 x 4096 x 14336: four 17.5 us, six
 // 16.5; up to 48 tokens 160 KB hold five, up to 64 four), or four with two row
 // tiles each, which halves the tokens where there are more tiles than units
 // (32 x 7168 x 7168: 17.4 us with one tile, 13.9 with two).
@@ -1681,7 +1682,7 @@ static hipError_t launch_type(LinearArgs a, hipStream_t s) {
     case kTileStream16:
     case kTileStream16Pair:
     case kTileStream32:
-        case kTileStream32Pair:
+    case kTileStream32Pair:
     case kTileStream48:
     case kTileStream64: return launch_stream<WT, OT>(a, s);
     case kTile256:

@@ -54,7 +54,7 @@ struct LinearArgs {
   void* wpack;
 };
 
-// At most this many tokens stream W (stream.h).
+// At most this many tokens stream W (stream.h); of int8, up to four times as many.
 constexpr int kLinStreamTokens = 16;
 
 // ------------------------------------------------------------ choice of kernel
@@ -239,7 +239,9 @@ inline void linear_plan(LinearArgs* a) {
 // to 12 GB, are what counts: 1%, at worst 23% (64 rows in 256 groups x 7168 x 2048:
 // 128 x 64 156 us, 64 x 64 188, 128 x 128 194).
 //
-// K is split only while every range has a place on the chip at once.
+// K is split into at most 512 workgroups in all, two for a compute unit, of any
+// tile (by groups: of the tiles to expect).  Tiles that are alone on their unit then
+// run in up to two rounds, which the estimate counts.
 struct Int8TileCost {
   int tile, rows, tokens, held;
   float fixed, start;  // us per stage apart from the bytes; per round

@@ -40,9 +40,12 @@ template <typename AT>
 struct NormRow {
   static constexpr int kN = 16 / (int)sizeof(AT);  // elements of a unit
 
-  // elements c .. c + kN - 1 of a row of d, zero past its end.  Rows are read
-  // once: nontemporal (8192 x 4096 bf16 to y and codes 51.7 -> 49.6 us; stores
-  // with the hint took 5% more in fp32)
+  // elements c .. c + kN - 1 of a row of d, zero past its end.  Rows that stay in
+  // registers are read once: nontemporal (8192 x 4096 bf16 to y and codes 51.7 ->
+  // 49.6 us; stores with the hint took 5% more in fp32).  Longer rows, which are
+  // read again, take the hint too; plain loads there, fp32: codes of 64 / 2048 x 32768
+  // 12.2 / 99 -> 8.0 / 93 us, but y of 256 x 131072 71 -> 79, and the gradient's first
+  // pass 4096 x 7168 without dsum 106 -> 111, bf16 2048 x 16384 with it 90 -> 87.
   static __device__ __forceinline__ u32x4 raw(const AT* row, int c, int d) {
     if (c + kN <= d)
       return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + c));
@@ -306,7 +309,8 @@ __global__ __launch_bounds__(NormGeom<kLanes>::kThreads) void norm_kernel(NormAr
 }
 
 // Rows that the registers of a workgroup do not hold: a workgroup per row
-// reads it again for every step (from the caches where it fits them).
+// reads it again for every step (fp32 to codes, 2048 x 32768: 99 us, one read and
+// the codes 67 at the rate of a copy; to y 127, 107).
 constexpr int kNormLong = 1024;
 template <typename AT, bool kNorm>
 __global__ __launch_bounds__(kNormLong) void norm_long_kernel(NormArgs a) {
@@ -630,7 +634,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 }
 
 // The gradient's geometries: its weights, shares of dweight and the next row
-// leave room for 16 bf16 or 8 fp32 of a row per lane.
+// leave room for 16 bf16 or 8 fp32 of a row per lane.  The widest has 512 lanes:
+// rows over 16 KiB are read twice (fp32 4096 x 7168 with dsum 128 us, 94 at the rate
+// of a copy; 4096 x 4096, held, 48 and 54).  1024 lanes with as much each, for rows
+// to 32 KiB, have not been built.
 template <typename F, typename L>
 static auto norm_backward_geometry(int cols, int act_dtype, const F& f, const L& longer) {
   const int size = act_dtype == kDtypeF32 ? 4 : 2;

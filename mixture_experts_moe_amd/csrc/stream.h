@@ -1,4 +1,4 @@
-// Weight streaming for a few tokens (at most 16): the matrix-vector end of a
+// Weight streaming for a few tokens (at most 16; int8 64): the matrix-vector end of a
 // product, bound by how fast the weight rows arrive.
 //
 // One load instruction takes four weight rows x 256 contiguous bytes: lane l
